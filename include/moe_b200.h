@@ -6,7 +6,8 @@
  *     z = x W_r,  p = softmax(z),  y = sum over top-k(p) of g_i FFN_i(x)
  * plus the capacity limit of section 3, the balancing losses of section 2 and
  * shared experts that run on every token.  Each stage is one call; moe_forward
- * runs them all.
+ * runs them all.  The experts' training calls (gradients, grouped products,
+ * orthogonalised updates) follow the forward's.
  *
  * Conventions for every call:
  *   - Pointers named x, W*, y, ... are DEVICE pointers unless marked "host".
@@ -474,6 +475,126 @@ moe_status moe_bias_update(const moe_config *cfg, const int32_t *counts, float g
 moe_status moe_forward(const moe_config *cfg, const moe_weights *w,
                        const void *x, const moe_outputs *out, void *ws,
                        size_t ws_bytes, moe_stream_t stream);
+
+/* ---- training the experts ------------------------------------------------
+ * Gradients of the calls above, the grouped products they are made of, and the
+ * orthogonalised update.  A segment table says which rows of a tall [R, .]
+ * buffer belong to group g (an expert): rows [offsets[g], offsets[g] + rows[g]),
+ * offsets [G + 1] int32 not decreasing, rows [G] int32 or NULL for
+ * offsets[g + 1] - offsets[g] (rows[g] is held to that span; the capacity
+ * stage's offsets and kept fit).  Both are device pointers; starts need no
+ * alignment and groups may be empty.  Entries outside [0, R] are held inside
+ * it.  Rows of no group are neither read into any result (they may hold NaN)
+ * nor written.
+ *
+ * bf16 runs on the tensor cores and accumulates in fp32; N and K are multiples
+ * of 8 there (16-byte rows, else MOE_ERR_SHAPE) and pointers 16-byte aligned.
+ * fp32 runs on the CUDA cores, any N and K.  1 <= G <= 256.  Every call takes a
+ * workspace whose first word is the device status word (cleared by the call),
+ * is safe to capture in a CUDA graph, and gives the same bits on every run. */
+
+/* Workspace bytes of the three grouped products; 0 for invalid arguments. */
+size_t moe_grouped_workspace_size(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K);
+
+/*
+ * moe_grouped_matmul - y[r] = W[g] x[r] for the rows r of each group g ("Lab 18"
+ * tips: one grouped matrix multiply over all experts), with no activation.
+ *   x [R, K], W [G, N, K], y [R, N], all of `dtype`.
+ */
+moe_status moe_grouped_matmul(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K,
+                              const void *x, const void *W, const int32_t *offsets,
+                              const int32_t *rows, void *y, void *ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/*
+ * moe_grouped_matmul_dx - its gradient by x: dx[r] = W[g]^T dy[r].
+ *   dy [R, N], W [G, N, K], dx [R, K], all of `dtype`; W is read as it lies.
+ */
+moe_status moe_grouped_matmul_dx(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K,
+                                 const void *dy, const void *W, const int32_t *offsets,
+                                 const int32_t *rows, void *dx, void *ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+
+/*
+ * moe_grouped_matmul_dw - its gradient by W:
+ *     dW[g] = (add[g] +) sum over the rows r of group g of dy[r] x[r]^T.
+ *   dy [R, N], x [R, K] of `dtype`; dW and add [G, N, K] of dw_dtype (fp32, or
+ *   bf16 when dtype is bf16).  add NULL: nothing is added, an empty group's dW
+ *   is zero.  add may be dW itself (gradients summed over micro-batches); the
+ *   sum is rounded once.
+ */
+moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K,
+                                 const void *dy, const void *x, const int32_t *offsets,
+                                 const int32_t *rows, int32_t dw_dtype, const void *add, void *dW,
+                                 void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_combine_backward - gradients of moe_combine ("Lab 18" section 1,
+ * y = sum g_i FFN_i(x)): for every kept (t, j) with r = offsets[e] + pos[t, j],
+ *     dY_perm[r] = gates[t, j] dy[t],   dgates[t, j] = <dy[t], Y_perm[r]>;
+ * dgates is 0 for dropped assignments, padding rows of dY_perm are left
+ * untouched.  The gradients by Y_shared and by the residual are dy itself; the
+ * gradient of moe_dispatch is moe_combine with unit gates.
+ *   dy [T, d], Y_perm, dY_perm [moe_perm_rows, d] dtype; dgates [T, k] fp32;
+ *   the rest as for moe_combine.
+ */
+moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *Y_perm,
+                                const float *gates, const int32_t *topk_idx, const int32_t *pos,
+                                const uint8_t *keep, const int32_t *offsets, void *dY_perm,
+                                float *dgates, moe_stream_t stream);
+
+/* Workspace bytes of moe_expert_ffn_backward (hidden activations and their
+ * gradients); 0 for an invalid configuration. */
+size_t moe_ffn_backward_workspace_size(const moe_config *cfg);
+
+/*
+ * moe_expert_ffn_backward - gradients of moe_expert_ffn.  The hidden
+ * activations are computed again from the inputs (nothing of the forward has to
+ * be kept but x_perm): with u = W1 x, v = W3 x, dh = W2^T dY,
+ *   GELU    h = gelu(u),    du = dh gelu'(u)
+ *   SwiGLU  h = silu(u) v,  du = dh v silu'(u),  dv = dh silu(u)
+ *   dx = W1^T du (+ W3^T dv);  dW1 = sum du x^T, dW3 = sum dv x^T, dW2 = sum dY h^T
+ * over the rows of each expert.  u, v and dh stay in fp32 accumulators (bf16);
+ * h, du and dv are rounded to dtype once.
+ *   x_perm, dY_perm [moe_perm_rows, d]; offsets [E + 1], kept [E] of the
+ *     capacity stage; dx_perm [moe_perm_rows, d] out (padding rows untouched).
+ *   x, dY_shared [T, d], Ws1, Ws3, Ws2 in and dx_shared [T, d], dWs1, dWs3, dWs2
+ *     out for the shared experts (all NULL when S = 0; S <= 64): dx_shared is
+ *     the sum over them.
+ *   dW* shaped like the weights, of dw_dtype (fp32, or bf16 in a bf16 layer);
+ *     accumulate 1 adds to what they hold.
+ *   ws: moe_ffn_backward_workspace_size bytes.
+ */
+moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
+                                   const int32_t *offsets, const int32_t *kept,
+                                   const void *dY_perm, const void *W1, const void *W3,
+                                   const void *W2, const void *x, const void *dY_shared,
+                                   const void *Ws1, const void *Ws3, const void *Ws2,
+                                   void *dx_perm, void *dW1, void *dW3, void *dW2,
+                                   void *dx_shared, void *dWs1, void *dWs3, void *dWs2,
+                                   int32_t dw_dtype, int32_t accumulate, void *ws,
+                                   size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace bytes of moe_orthogonalize; 0 for invalid arguments. */
+size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t steps);
+
+/*
+ * moe_orthogonalize - each expert's update with its singular values driven
+ * towards 1: X = G[e] / (|G[e]|_F + eps), then `steps` times A = X X^T and
+ * X = a X + (b A + c A A) X (X^T X from the right when m > n), U[e] = scale X.
+ *   G [E, m, n] fp32 or bf16 (`dtype`), any alignment of its elements; U
+ *   [E, m, n] bf16.  coeffs (host): a, b, c; they must keep the singular values
+ *   below 2.8 and those of b A + c A A below 16, as 3.4445, -4.775, 2.0315 or
+ *   1.5, -0.5, 0 do (fp16 intermediates).  1 <= E <= 1024, m, n <= 2^20, 1 <=
+ *   steps <= 32.  A matrix of zeros gives zeros; one with an infinity or NaN
+ *   gives NaN, in its own update only.
+ * Intermediates are pairs of fp16 terms except in the last step: the result is
+ * that of 64-bit arithmetic within about 1e-3 (relative, 2-norm), then rounded
+ * to bf16.
+ */
+moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, const void *G,
+                             int32_t steps, const float *coeffs, float eps, float scale, void *U,
+                             void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * moe_device_status - read the device status word that the bounded waits of

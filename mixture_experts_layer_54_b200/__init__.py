@@ -1,4 +1,5 @@
-"""Token-choice Mixture-of-Experts forward pass for NVIDIA B200 (sm_100a).
+"""Token-choice Mixture-of-Experts layer for NVIDIA B200 (sm_100a): the forward
+pass, and the gradients and updates that train its experts.
 
 The work happens in libmoe_b200.so (CUDA kernels behind the C ABI of
 include/moe_b200.h); this package is its ctypes binding.  Importing the ops
@@ -16,6 +17,9 @@ from .ops import (CapacityOut, HostStream, MoEForward, moe_bias_update, moe_capa
                   moe_stage_workspace_size, moe_validate, moe_workspace_size, weights_struct,
                   StagedForward,
                   workspace)
+from .training import (FFNGrads, moe_combine_backward, moe_expert_ffn_backward,
+                       moe_ffn_backward_workspace_size, moe_grouped_matmul, moe_grouped_matmul_dw,
+                       moe_grouped_matmul_dx, moe_orthogonalize, moe_orthogonalize_workspace_size)
 
 __all__ = ["MOE_ROW_ALIGN", "CapacityFactorError", "MoEError", "MoeConfig", "MoeOutputs",
            "MoeWeights", "LIB_PATH", "lib", "CapacityOut", "HostStream", "MoEForward", "moe_bias_update",
@@ -26,4 +30,7 @@ __all__ = ["MOE_ROW_ALIGN", "CapacityFactorError", "MoEError", "MoeConfig", "Moe
            "moe_combine", "moe_config", "moe_device_status", "moe_dispatch", "moe_expert_ffn",
            "moe_forward", "moe_loss_partials_count", "moe_losses", "moe_perm_rows", "moe_route",
            "moe_stage_workspace_size", "moe_validate", "moe_workspace_size", "weights_struct",
-           "workspace", "StagedForward"]
+           "workspace", "StagedForward", "FFNGrads", "moe_combine_backward",
+           "moe_expert_ffn_backward", "moe_ffn_backward_workspace_size", "moe_grouped_matmul",
+           "moe_grouped_matmul_dw", "moe_grouped_matmul_dx", "moe_orthogonalize",
+           "moe_orthogonalize_workspace_size"]

@@ -43,6 +43,7 @@ class MoeOutputs(ctypes.Structure):
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoeConfig)
+_GROUPED = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_validate": (ctypes.c_int, [_CFG]),
@@ -76,6 +77,19 @@ SIGNATURES = {
     "moe_losses": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P]),
     "moe_forward": (ctypes.c_int, [_CFG, ctypes.POINTER(MoeWeights), _P,
                                    ctypes.POINTER(MoeOutputs), _P, ctypes.c_size_t, _P]),
+    "moe_grouped_workspace_size": (ctypes.c_size_t, _GROUPED),
+    "moe_grouped_matmul": (ctypes.c_int, _GROUPED + [_P] * 6 + [ctypes.c_size_t, _P]),
+    "moe_grouped_matmul_dx": (ctypes.c_int, _GROUPED + [_P] * 6 + [ctypes.c_size_t, _P]),
+    "moe_grouped_matmul_dw": (ctypes.c_int, _GROUPED + [_P] * 4 + [ctypes.c_int32] + [_P] * 3 +
+                              [ctypes.c_size_t, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_CFG] + [_P] * 10),
+    "moe_ffn_backward_workspace_size": (ctypes.c_size_t, [_CFG]),
+    "moe_expert_ffn_backward": (ctypes.c_int, [_CFG] + [_P] * 20 +
+                                [ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "moe_orthogonalize_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "moe_orthogonalize": (ctypes.c_int, [ctypes.c_int32] * 4 +
+                          [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_float), ctypes.c_float,
+                           ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
     "moe_device_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_clear_device_status": (ctypes.c_int, [_P, _P]),
     "moe_probe_wait_timeout": (ctypes.c_int, [_P, ctypes.c_uint64, _P]),

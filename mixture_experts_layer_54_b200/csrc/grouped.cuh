@@ -1,0 +1,93 @@
+// Grouped matrix products shared by the expert training calls: what a launch
+// is told (grouped_tc.cu runs it on the tensor cores, grouped_simt.cu in fp32).
+#pragma once
+
+#include "internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace grp {
+
+// Which extent of a group the segment table gives.
+//   RAGGED_M: its output rows are rows [offsets[g], offsets[g] + rows[g]) of
+//             one tall buffer (products with the expert's weights);
+//   RAGGED_K: its contraction runs over those rows (weight gradients);
+//   DENSE:    every group has the same extents (shared experts, stacks).
+enum Mode { RAGGED_M = 0, RAGGED_K = 1, DENSE = 2 };
+
+constexpr int kSets = 6;
+constexpr int kEntries = 1024;   // (set, group) pairs of a launch
+
+// One family of products of a launch: out[g] = sum over K segments of A B^T.
+struct Set {
+    // Segment i of a tile's contraction multiplies operand pair i % period:
+    // A map (seg_a >> i % period) & 1, B map (seg_b >> i % period) & 1; with
+    // seg_grouped both operands' group is i / period.
+    CUtensorMap a[2], b[2];
+    CUtensorMap b3;              // EPI_SWIGLU: W3 (b[0] = W1, b[1] = W2)
+    int mode, groups, ent0;      // ent0: first entry of the tile table
+    int M, N, K;                 // output rows (not RAGGED_M), columns, contraction (not RAGGED_K)
+    int segs, period, seg_a, seg_b, seg_grouped;
+    int a_grouped, b_grouped;    // 1: the operand has one matrix per group
+    int sym;                     // 1: out is symmetric; only tiles on or below the diagonal
+    int ld;                      // row pitch of out (elements)
+    int64_t out_group;           // elements between the groups' outputs (not RAGGED_M)
+    void *out;                   // EPI_GELU / EPI_SWIGLU: h
+    void *out2, *out3;           // EPI_GELU / EPI_SWIGLU: du, dv; EPI_NS: out2 = low halves
+    const void *add;             // EPI_DW, nullable: added before the rounding
+    int out_f32;                 // EPI_DW
+    // EPI_NS: val = alpha acc + beta base; see orthogonalize.cu
+    const void *base, *base2;    // nullable high and low halves, at the transposed place if base_t
+    int base_ld, base_t, out_bf16;
+    int64_t base_group;
+    float alpha, beta;
+    const float *scale;          // nullable: scale[g] divides as scale_pow says
+    int scale_pow;               // val = alpha / s^pow acc + beta / s base (s once for pow < 2)
+    int vec;                     // 1: 16-byte rows (out aligned, ld a multiple of 8)
+};
+
+struct __align__(64) Params {
+    Set set[kSets];
+    int nsets, entries;
+    const int32_t *offsets;      // [G + 1]
+    const int32_t *rows;         // [G], nullable: offsets[g + 1] - offsets[g]
+    int n_rows;                  // rows of the tall buffers; the table is held inside them
+    int fp16;                    // operands are fp16 (else bf16)
+    int32_t *status;
+    int clear_status;
+    unsigned long long timeout_ns;
+};
+
+// First row and row count of group g, held inside the buffers whatever the
+// table says.
+__device__ __forceinline__ void group_rows(const int32_t *offsets, const int32_t *rows, int n_rows,
+                                           int g, int *start, int *count)
+{
+    const int lo = min(max(offsets[g], 0), n_rows), hi = min(max(offsets[g + 1], lo), n_rows);
+    *start = lo;
+    *count = rows ? min(max(rows[g], 0), hi - lo) : hi - lo;
+}
+
+// Epilogues: EPI_ROWS bf16 rows; EPI_DW fp32 or bf16 with an addend; EPI_NS
+// the Newton-Schulz stores; EPI_GELU / EPI_SWIGLU the hidden activations and
+// their gradients.
+enum Epi { EPI_ROWS = 0, EPI_DW = 1, EPI_NS = 2, EPI_GELU = 3, EPI_SWIGLU = 4 };
+
+// Operand layouts: MN = the contraction index is the row index of the stored
+// matrix (its other index is contiguous), K = the contraction is contiguous.
+enum Layout { A_K_B_K = 0, A_K_B_MN = 1, A_MN_B_MN = 2 };
+
+// Launches with `pair` 1 for 256-row SM-pair tiles, 0 for 128-row tiles.
+cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t s);
+
+// Maps of a [groups, rows, cols] 2-byte tensor with row pitch ld for the
+// operand's role (group_stride in elements).
+bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
+           int64_t groups, int64_t group_stride, int box_rows);
+bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
+            int64_t groups, int64_t group_stride);
+// Rows of the B box of a K-major operand in launches of this shape.
+int b_box_rows(Epi epi, bool pair);
+
+}  // namespace grp
+}  // namespace moe

@@ -1,0 +1,905 @@
+// Grouped matrix products on the 5th-generation tensor cores, for operands of
+// either storage order: y = x W^T, dx = dy W, dW = dy^T x over the ragged
+// expert segments, the hidden gradients of the expert FFNs, and the stacked
+// products of the Newton-Schulz steps.
+//
+// One persistent, warp-specialised kernel (TMA -> shared memory ->
+// tcgen05.mma -> TMEM -> registers -> global).  PAIR tiles take a 2-CTA
+// cluster: 256 output rows (128 a CTA) x BN columns, each CTA loading its rows
+// of A and half the rows of B.  Operands whose contraction index is the row
+// index of the stored matrix (W in dx, both in dW) are read as they lie: boxes
+// of 64 contiguous elements x 64 contraction rows, and the MMA takes them as
+// MN-major, so nothing is transposed in memory.
+//
+// Ragged contractions (dW): a group's rows end anywhere, and what follows
+// belongs to the next group or to nobody (it may hold NaN, so it cannot be
+// multiplied by zeros).  The MMA stops at the 16-row step holding the last
+// row; the producer waits for that box and clears the up to 15 rows behind it
+// in shared memory before handing the stage over.
+//
+// Output rows go through a 2 KB staging tile per epilogue warp to 64-byte
+// pieces of rows, each masked by the group's end: rows behind it are neither
+// written nor read.
+//
+// Roles: warp 0 loads, warp 1 issues the MMAs (and owns TMEM), warps 2..9 are
+// the epilogue (warp w reads TMEM lanes 32 (w mod 4) .. +31, warps 2..5 the
+// first half of the columns).  Every wait is bounded; on expiry the CTA sets
+// MOE_ERR_DEVICE_TIMEOUT, every role leaves its loop, copies in flight are
+// awaited (bounded too), TMEM is freed and the kernel returns.
+#include "grouped.cuh"
+
+#include <cuda_fp16.h>
+#include <string.h>
+
+namespace moe {
+namespace grp {
+
+using namespace tc;
+
+namespace {
+
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int A_BYTES = 128 * 128;       // 128 rows x 64 elements of one CTA
+constexpr int STG_WARP = 32 * 64;        // staging tile of an epilogue warp: 32 rows x 64 bytes
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int RING_BYTES = 192 * 1024;
+
+template <int CTAS, int BN, int EPI>
+struct Shape {
+    static constexpr bool ACT = EPI == EPI_GELU || EPI == EPI_SWIGLU;
+    static constexpr int BM = 128 * CTAS;
+    // accumulator columns of the widest B tile (ACT: u, with v beside it)
+    static constexpr int BNB = EPI == EPI_SWIGLU ? 2 * BN : BN;
+    static constexpr int B_ROWS = BNB / CTAS;            // B rows of one CTA
+    static constexpr int B_BYTES = B_ROWS * 128;         // of 64 contraction elements
+    static constexpr int SUB = A_BYTES + B_BYTES;
+    // 128 of K a stage where three stages fit: half the barrier round trips
+    static constexpr int KSUB = 6 * SUB <= RING_BYTES ? 2 : 1;
+    static constexpr int STAGES = RING_BYTES / (KSUB * SUB) > 6 ? 6 : RING_BYTES / (KSUB * SUB);
+    static constexpr int BK = 64 * KSUB;
+    static constexpr int OFF_B = STAGES * KSUB * A_BYTES;
+    static constexpr int OFF_STG = OFF_B + STAGES * KSUB * B_BYTES;
+    static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * STG_WARP;
+    static constexpr int OFF_TAB = OFF_BAR + 256;
+    static constexpr int SMEM = OFF_TAB + 4 * (kEntries + 1) + 1024;   // + alignment slack
+    // TMEM columns.  Plain: two accumulators of BN.  GELU: u and dh, twice.
+    // SwiGLU: u | v once (256 columns), dh twice behind it.
+    static constexpr int DH_COL = EPI == EPI_SWIGLU ? 2 * BN : BN;
+};
+
+struct Tile {
+    int set, g;
+    int m0, n0;        // first output row (in the group) and column
+    int mg;            // output rows of the group
+    int row0;          // first row of the group in the tall buffers (RAGGED_M)
+    int k0, klen;      // contraction: first index and length
+};
+
+// Tiles of entry (set, g).
+template <int BM, int BN>
+__device__ __forceinline__ int entry_tiles(const Params &p, const Set &s, int g)
+{
+    int m = s.M;
+    if (s.mode == RAGGED_M) {
+        int start;
+        group_rows(p.offsets, p.rows, p.n_rows, g, &start, &m);
+    }
+    const int mt = (m + BM - 1) / BM, nt = (s.N + BN - 1) / BN;
+    if (!s.sym)
+        return mt * nt;
+    int n = 0;
+    for (int i = 0; i < mt; ++i)
+        n += min(nt, (i + 1) * (BM / BN));
+    return n;
+}
+
+template <int BM, int BN>
+__device__ __forceinline__ Tile decode(const Params &p, const int *tstart, int tile)
+{
+    int lo = 0, hi = p.entries;   // last entry with tstart <= tile
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tstart[mid] <= tile)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Tile t;
+    int set = 0;
+    while (set + 1 < p.nsets && p.set[set + 1].ent0 <= lo)
+        ++set;
+    const Set &s = p.set[set];
+    t.set = set;
+    t.g = lo - s.ent0;
+    t.mg = s.M;
+    t.row0 = 0;
+    t.k0 = 0;
+    t.klen = s.K;
+    if (s.mode == RAGGED_M)
+        group_rows(p.offsets, p.rows, p.n_rows, t.g, &t.row0, &t.mg);
+    else if (s.mode == RAGGED_K)
+        group_rows(p.offsets, p.rows, p.n_rows, t.g, &t.k0, &t.klen);
+    int i = tile - tstart[lo];
+    const int nt = (s.N + BN - 1) / BN;
+    if (s.sym) {
+        int r = 0;
+        for (;; ++r) {
+            const int c = min(nt, (r + 1) * (BM / BN));
+            if (i < c)
+                break;
+            i -= c;
+        }
+        t.m0 = r * BM;
+        t.n0 = i * BN;
+    } else {
+        const int mt = (t.mg + BM - 1) / BM;
+        t.m0 = (i % mt) * BM;
+        t.n0 = (i / mt) * BN;
+    }
+    return t;
+}
+
+// MN-major operand, 128-byte swizzle: 64 contiguous elements per 128-byte row,
+// one row per contraction index; 8-row groups 1024 bytes apart (stride offset),
+// blocks of 64 elements 8192 bytes apart (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate)
+{
+    if (CTAS == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void commit_all(uint32_t bar)
+{
+    if (CTAS == 2)
+        mma_commit_pair(bar);
+    else
+        mma_commit(bar);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0,
+                                         int c1, int c2)
+{
+    if (CTAS == 2)
+        tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+    else
+        tma_load_3d(dst, m, bar, c0, c1, c2);
+}
+
+// arrive (with `bytes` more to come, if any) on the leader's barrier
+template <int CTAS>
+__device__ __forceinline__ void arrive_leader(uint32_t bar, uint32_t bytes)
+{
+    if (CTAS == 2)
+        asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::
+                         "r"(bar),
+                     "r"(bytes)
+                     : "memory");
+    else
+        mbar_expect_tx(bar, bytes);
+}
+
+// 32 columns of packed 16-bit values of this lane's row -> rows of the output.
+// dst: row 0, column 0 of the piece; rv rows and cv columns of it are stored.
+__device__ __forceinline__ void store16(uint8_t *stg, int lane, const uint32_t *packed,
+                                        uint16_t *dst, int64_t ld, int rv, int cv, int vec)
+{
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(packed[4 * ch], packed[4 * ch + 1], packed[4 * ch + 2],
+                       packed[4 * ch + 3]);
+    __syncwarp();
+    if (vec) {
+        const int ch = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            if (r < rv && ch * 8 < cv)
+                *reinterpret_cast<uint4 *>(dst + r * ld + ch * 8) =
+                    *reinterpret_cast<const uint4 *>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+        }
+    } else {
+        for (int r = 0; r < min(rv, 32); ++r)
+            if (lane < cv)
+                dst[r * ld + lane] = *reinterpret_cast<const uint16_t *>(
+                    stg + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+    }
+}
+
+// 16 fp32 columns of this lane's row, plus the addend, to fp32 or bf16 rows.
+__device__ __forceinline__ void store_dw(uint8_t *stg, int lane, const float *v, const Set &s,
+                                         int64_t at, int rv, int cv)
+{
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        *reinterpret_cast<float4 *>(stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+            make_float4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
+    __syncwarp();
+    const int ch = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        if (r >= rv || ch * 4 >= cv)
+            continue;
+        float4 f = *reinterpret_cast<const float4 *>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+        const int64_t o = at + (int64_t)r * s.ld + ch * 4;
+        if (s.out_f32) {
+            if (s.add) {
+                const float4 a = *reinterpret_cast<const float4 *>(
+                    static_cast<const float *>(s.add) + o);
+                f.x += a.x, f.y += a.y, f.z += a.z, f.w += a.w;
+            }
+            *reinterpret_cast<float4 *>(static_cast<float *>(s.out) + o) = f;
+        } else {
+            if (s.add) {
+                const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162 *>(
+                    static_cast<const __nv_bfloat16 *>(s.add) + o);
+                const float2 a0 = __bfloat1622float2(a[0]), a1 = __bfloat1622float2(a[1]);
+                f.x += a0.x, f.y += a0.y, f.z += a1.x, f.w += a1.y;
+            }
+            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(f.x, f.y), __floats2bfloat162_rn(f.z, f.w)};
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(s.out) + o) =
+                *reinterpret_cast<uint2 *>(h);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_fp16(float a, float b)
+{
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_fp16(uint32_t u)
+{
+    return __half22float2(*reinterpret_cast<__half2 *>(&u));
+}
+
+// val = alpha acc + beta base for 32 columns of this lane's row.  base_t reads
+// the (symmetric) base at the transposed place, where a column is contiguous
+// over the warp's rows.
+__device__ __forceinline__ void ns_values(const Set &s, int g, float alpha, float beta, int row,
+                                          int col, int rv, int cv, int lane, float *v)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] *= alpha;
+    if (!s.base || lane >= rv)
+        return;
+    const int64_t g0 = (int64_t)g * s.base_group;
+    const __half *hi = static_cast<const __half *>(s.base) + g0;
+    const __half *lo = s.base2 ? static_cast<const __half *>(s.base2) + g0 : nullptr;
+    if (s.base_t) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i < cv) {
+                const int64_t o = (int64_t)(col + i) * s.base_ld + row;
+                float b = __half2float(hi[o]);
+                if (lo)
+                    b += __half2float(lo[o]);
+                v[i] += beta * b;
+            }
+        }
+    } else {
+        const int64_t o = (int64_t)row * s.base_ld + col;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c * 8 >= cv)
+                continue;
+            // the pitch is a multiple of 8 and holds at least cv rounded up to it
+            const uint4 h = *reinterpret_cast<const uint4 *>(hi + o + 8 * c);
+            const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_fp16(w[j]);
+                v[8 * c + 2 * j] += beta * f.x;
+                v[8 * c + 2 * j + 1] += beta * f.y;
+            }
+            if (lo) {
+                const uint4 l = *reinterpret_cast<const uint4 *>(lo + o + 8 * c);
+                const uint32_t x[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack_fp16(x[j]);
+                    v[8 * c + 2 * j] += beta * f.x;
+                    v[8 * c + 2 * j + 1] += beta * f.y;
+                }
+            }
+        }
+    }
+}
+
+template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_constant__ Params p)
+{
+    using S = Shape<CTAS, BN, EPI>;
+    constexpr bool ACT = S::ACT;
+    constexpr int STAGES = S::STAGES, KSUB = S::KSUB, BM = S::BM;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    const uint32_t sA = smem_u32(smem), sB = smem_u32(smem + S::OFF_B);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    const uint32_t tail_bar = bar0 + 8u * (2 * STAGES + 5);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + 8 * (2 * STAGES + 6));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *tstart = reinterpret_cast<int *>(smem + S::OFF_TAB);   // [entries + 1]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
+    const bool leader = rank == 0;
+    const int unit = blockIdx.x / CTAS, units = gridDim.x / CTAS;
+    const Ctl ctl{abort_flag, p.status, p.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), CTAS);   // each CTA's producer, with its bytes
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), CTAS * EPI_WARPS);
+        }
+        mbar_init(drain_bar, 1);
+        mbar_init(tail_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        if (CTAS == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0)
+        *p.status = 0;
+    if (warp == 2) {
+        // tile table: running sum of the entries' tiles
+        int base = 0;
+        for (int e0 = 0; e0 < p.entries; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.entries) {
+                int set = 0;
+                while (set + 1 < p.nsets && p.set[set + 1].ent0 <= e)
+                    ++set;
+                n = entry_tiles<BM, BN>(p, p.set[set], e - p.set[set].ent0);
+            }
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d)
+                    sum += o;
+            }
+            if (e < p.entries)
+                tstart[e] = base + sum - n;
+            base += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0)
+            tstart[p.entries] = base;
+    }
+    tc_fence_before();
+    if (CTAS == 2)
+        cluster_sync();   // barriers initialised in both CTAs, TMEM allocated, table ready
+    else
+        __syncthreads();
+    tc_fence_after();
+    const int total = tstart[p.entries];
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        // ================= loads (both CTAs) =================
+        int stage = 0;
+        uint32_t phase = 0, tail_phase = 0;
+        int issued = 0;
+        uint32_t last_phase = 0;   // bit s: phase of stage s's last use
+        bool ok = true;
+        for (int tile = unit; ok && tile < total; tile += units) {
+            const Tile t = decode<BM, BN>(p, tstart, tile);
+            const Set &s = p.set[t.set];
+            const int m_row = t.m0 + (int)rank * 128 + (s.mode == RAGGED_M ? t.row0 : 0);
+            const int segs = ACT ? 2 : s.segs;
+            for (int sg = 0; ok && sg < segs; ++sg) {
+                const int ph = ACT ? sg : sg % s.period;
+                const int ai = ACT ? sg : (s.seg_a >> ph) & 1;
+                const int bi = ACT ? 1 - sg : (s.seg_b >> ph) & 1;
+                const int grp = !ACT && s.seg_grouped ? sg / s.period : t.g;
+                const int ga = s.a_grouped ? grp : 0, gb = s.b_grouped ? grp : 0;
+                const bool uv = EPI == EPI_SWIGLU && sg == 1;
+                const bool b_mn = ACT ? sg == 0 : B_MN;
+                // B rows of this CTA, and their first
+                const int b_rows = ACT ? (uv ? S::B_ROWS : BN / CTAS) : S::B_ROWS;
+                const int b_row = t.n0 + (uv && CTAS == 2 ? 0 : (int)rank * (BN / CTAS));
+                const CUtensorMap *am = &s.a[ai];
+                const CUtensorMap *bm = uv && rank == 1 ? &s.b3 : &s.b[bi];
+                for (int kb = 0; kb * S::BK < t.klen; ++kb) {
+                    int okw = lane == 0 ? (wait_bar(empty_bar(stage), phase ^ 1u, ctl) ? 1 : 0) : 1;
+                    if (!__shfl_sync(0xffffffffu, okw, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    const int rem = t.klen - kb * S::BK;
+                    const int nks = rem >= S::BK ? KSUB : (rem + 63) / 64;
+                    const uint32_t bytes = (uint32_t)nks * (A_BYTES + b_rows * 128);
+                    const uint32_t fb = CTAS == 2 ? map_to_rank(full_bar(stage), 0)
+                                                  : full_bar(stage);
+                    // rows behind the group's last must be cleared before use
+                    const bool tail = A_MN && s.mode == RAGGED_K && rem < S::BK && (rem & 15);
+                    if (lane == 0) {
+                        if (tail)
+                            mbar_expect_tx(tail_bar, bytes);
+                        else
+                            arrive_leader<CTAS>(fb, bytes);
+                        for (int ks = 0; ks < nks; ++ks) {
+                            const int kc = t.k0 + kb * S::BK + ks * 64;
+                            const uint32_t da = sA + (stage * KSUB + ks) * A_BYTES;
+                            const uint32_t db = sB + (stage * KSUB + ks) * S::B_BYTES;
+                            auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1,
+                                            int c2) {
+                                if (tail)
+                                    tma_load_3d(dst, m, tail_bar, c0, c1, c2);
+                                else
+                                    load_box<CTAS>(dst, m, fb, c0, c1, c2);
+                            };
+                            if (A_MN) {
+                                load(da, am, m_row, kc, ga);
+                                load(da + 8192, am, m_row + 64, kc, ga);
+                            } else {
+                                load(da, am, kc, m_row, ga);
+                            }
+                            if (b_mn) {
+                                for (int b = 0; b < b_rows / 64; ++b)
+                                    load(db + b * 8192, bm, b_row + b * 64, kc, gb);
+                            } else if (uv && CTAS == 1) {
+                                load(db, bm, kc, b_row, gb);
+                                load(db + BN * 128, &s.b3, kc, b_row, gb);
+                            } else {
+                                load(db, bm, kc, b_row, gb);
+                            }
+                        }
+                    }
+                    if (tail) {
+                        okw = lane == 0 ? (wait_bar(tail_bar, tail_phase, ctl, false) ? 1 : 0) : 1;
+                        okw = __shfl_sync(0xffffffffu, okw, 0);
+                        tail_phase ^= 1u;
+                        const int ks = (rem - 1) / 64, r0 = rem - ks * 64;
+                        const int n = (16 - (r0 & 15)) * 8;   // 16-byte pieces per 64-wide box
+                        const uint32_t da = sA + (stage * KSUB + ks) * A_BYTES + r0 * 128;
+                        const uint32_t db = sB + (stage * KSUB + ks) * S::B_BYTES + r0 * 128;
+                        const int boxes = 2 + b_rows / 64;
+                        for (int i = lane; i < n * boxes; i += 32) {
+                            const int box = i / n;
+                            const uint32_t dst =
+                                (box < 2 ? da + box * 8192 : db + (box - 2) * 8192) + (i % n) * 16;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst),
+                                         "r"(0)
+                                         : "memory");
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            arrive_leader<CTAS>(fb, 0);
+                        if (!okw) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    issued |= 1 << stage;
+                    last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        // the leader's full barriers count both CTAs' bytes: drain there
+        if (leader && lane == 0)
+            for (int s = 0; s < STAGES; ++s)
+                if (issued >> s & 1)
+                    wait_bar<true>(full_bar(s), last_phase >> s & 1, ctl, false);
+    } else if (warp == 1) {
+        // ================= MMA issue (leader CTA only) =================
+        if (lane == 0 && leader) {
+            const uint32_t fmt = p.fp16 ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t idesc0 = (1u << 4) | fmt | ((uint32_t)(BM >> 4) << 24);
+            int stage = 0;
+            uint32_t phase = 0;
+            int it = 0;
+            bool ok = true, any = false;
+            for (int tile = unit; ok && tile < total; tile += units, ++it) {
+                const Tile t = decode<BM, BN>(p, tstart, tile);
+                const Set &s = p.set[t.set];
+                const int slot = it & 1;
+                if (!wait_bar(tempty_bar(slot), ((it >> 1) & 1) ^ 1u, ctl)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int segs = ACT ? 2 : s.segs;
+                bool first = true;
+                for (int sg = 0; ok && sg < segs; ++sg) {
+                    const bool uv = EPI == EPI_SWIGLU && sg == 1;
+                    const bool b_mn = ACT ? sg == 0 : B_MN;
+                    uint32_t d = tmem_base;
+                    if (!ACT)
+                        d += slot * BN;
+                    else if (EPI == EPI_GELU)
+                        d += slot * 2 * BN + (sg == 0 ? S::DH_COL : 0);
+                    else
+                        d += sg == 0 ? S::DH_COL + slot * BN : 0;
+                    if (ACT)
+                        first = true;
+                    if (uv && it > 0) {
+                        // u | v has one slot: the previous tile's epilogue must be done
+                        if (!wait_bar(tempty_bar(slot ^ 1), ((it - 1) >> 1) & 1, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    const uint32_t idesc = idesc0 | (A_MN ? 1u << 15 : 0u) |
+                                           (b_mn ? 1u << 16 : 0u) |
+                                           ((uint32_t)((uv ? 2 * BN : BN) >> 3) << 17);
+                    for (int kb = 0; kb * S::BK < t.klen; ++kb) {
+                        if (!wait_bar<true>(full_bar(stage), phase, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const int rem = t.klen - kb * S::BK;
+                        const int steps = rem >= S::BK ? S::BK / 16 : (rem + 15) / 16;
+#pragma unroll
+                        for (int st = 0; st < S::BK / 16; ++st) {
+                            if (st >= steps)
+                                break;
+                            const int ks = st >> 2, kk = st & 3;
+                            const uint32_t a = sA + (stage * KSUB + ks) * A_BYTES;
+                            const uint32_t b = sB + (stage * KSUB + ks) * S::B_BYTES;
+                            mma<CTAS>(d, A_MN ? sdesc_mn(a + kk * 2048) : sdesc_sw128(a + kk * 32),
+                                      b_mn ? sdesc_mn(b + kk * 2048) : sdesc_sw128(b + kk * 32),
+                                      idesc, first ? 0u : 1u);
+                            first = false;
+                        }
+                        commit_all<CTAS>(empty_bar(stage));
+                        any = true;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                if (!ok)
+                    break;
+                commit_all<CTAS>(tfull_bar(slot));
+                any = true;
+            }
+            if (any) {
+                if (CTAS == 2)
+                    mma_commit_local2(drain_bar);
+                else
+                    mma_commit(drain_bar);
+                wait_bar(drain_bar, 0, ctl, false);
+            }
+        }
+    } else {
+        // ================= epilogue (warps 2..9, both CTAs) =================
+        const int q = warp & 3, ew = warp - 2, half = ew >> 2;
+        uint8_t *stg = smem + S::OFF_STG + ew * STG_WARP;
+        int it = 0;
+        for (int tile = unit; tile < total; tile += units, ++it) {
+            const Tile t = decode<BM, BN>(p, tstart, tile);
+            const Set &s = p.set[t.set];
+            const int slot = it & 1;
+            if (!wait_bar(tfull_bar(slot), (it >> 1) & 1, ctl))
+                break;
+            tc_fence_after();
+            const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
+            const int m = t.m0 + (int)rank * 128 + q * 32;   // first row, in the group
+            const int rv = t.mg - m;                          // rows of it from there on
+            const int c_end = rv > 0 ? min((half + 1) * (BN / 2), s.N - t.n0) : 0;
+            const int64_t row = m + (s.mode == RAGGED_M ? t.row0 : 0);
+            const int64_t at0 = (s.mode == RAGGED_M ? 0 : (int64_t)t.g * s.out_group) +
+                                row * s.ld + t.n0;
+#pragma unroll 1
+            for (int c = half * (BN / 2); c < c_end; c += 32) {
+                const int cv = s.N - t.n0 - c;
+                const int64_t at = at0 + c;
+                float v[32];
+                uint32_t w[16];
+                if constexpr (ACT) {
+                    // u = x W1^T, v = x W3^T, dh = dy W2; h = act(u) (v), and the
+                    // gradients of u and v:
+                    //   GELU    h = u Phi(u); du = dh (Phi(u) + u phi(u))
+                    //   SwiGLU  h = u s v, s = 1 / (1 + e^-u);
+                    //           du = dh v s (1 + u (1 - s)), dv = dh u s
+                    const uint32_t tu = tq + c + (EPI == EPI_GELU ? slot * 2 * BN : 0);
+                    const uint32_t tdh = tq + c + S::DH_COL + slot * (EPI == EPI_GELU ? 2 * BN : BN);
+                    float dh[32];
+                    tmem_ld32(tu, v);
+                    tmem_ld32(tdh, dh);
+                    if constexpr (EPI == EPI_GELU) {
+                        uint32_t g[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float h[2], du[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float u = v[i + j];
+                                const float cdf = 0.5f * (1.f + erff(u * 0.70710678118654752f));
+                                h[j] = u * cdf;
+                                du[j] = dh[i + j] *
+                                        (cdf + u * 0.39894228040143268f * __expf(-0.5f * u * u));
+                            }
+                            w[i / 2] = pack_bf16(h[0], h[1]);
+                            g[i / 2] = pack_bf16(du[0], du[1]);
+                        }
+                        store16(stg, lane, w, static_cast<uint16_t *>(s.out) + at, s.ld, rv, cv, 1);
+                        store16(stg, lane, g, static_cast<uint16_t *>(s.out2) + at, s.ld, rv, cv, 1);
+                    } else {
+                        float x3[32];
+                        tmem_ld32(tu + BN, x3);
+                        uint32_t g[16], k[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float h[2], du[2], dv[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float u = v[i + j];
+                                const float sg = __fdividef(1.f, 1.f + __expf(-u));
+                                const float us = u * sg;
+                                h[j] = us * x3[i + j];
+                                dv[j] = dh[i + j] * us;
+                                du[j] = dh[i + j] * x3[i + j] * (sg + us * (1.f - sg));
+                            }
+                            w[i / 2] = pack_bf16(h[0], h[1]);
+                            g[i / 2] = pack_bf16(du[0], du[1]);
+                            k[i / 2] = pack_bf16(dv[0], dv[1]);
+                        }
+                        store16(stg, lane, w, static_cast<uint16_t *>(s.out) + at, s.ld, rv, cv, 1);
+                        store16(stg, lane, g, static_cast<uint16_t *>(s.out2) + at, s.ld, rv, cv, 1);
+                        store16(stg, lane, k, static_cast<uint16_t *>(s.out3) + at, s.ld, rv, cv, 1);
+                    }
+                } else {
+                    tmem_ld32(tq + slot * BN + c, v);
+                    if (t.klen == 0) {   // nothing was accumulated: an empty group's sum
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = 0.f;
+                    }
+                    if constexpr (EPI == EPI_ROWS) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                        store16(stg, lane, w, static_cast<uint16_t *>(s.out) + at, s.ld, rv, cv, 1);
+                    } else if constexpr (EPI == EPI_DW) {
+                        store_dw(stg, lane, v, s, at, rv, cv);
+                        store_dw(stg, lane, v + 16, s, at + 16, rv, cv - 16);
+                    } else {
+                        float alpha = s.alpha, beta = s.beta;
+                        if (s.scale) {
+                            const float sc = s.scale[t.g];
+                            alpha = s.scale_pow == 2 ? alpha / sc / sc : alpha / sc;
+                            beta /= sc;
+                        }
+                        ns_values(s, t.g, alpha, beta, m + lane, t.n0 + c, rv, cv, lane, v);
+                        uint16_t *hi = static_cast<uint16_t *>(s.out) + at;
+                        if (s.out_bf16) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                            store16(stg, lane, w, hi, s.ld, rv, cv, s.vec);
+                            continue;
+                        }
+                        uint32_t lw[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            w[i] = pack_fp16(v[2 * i], v[2 * i + 1]);
+                            const float2 f = unpack_fp16(w[i]);
+                            lw[i] = pack_fp16(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+                        }
+                        // columns past N up to the pitch's multiple of 8 are written too
+                        const int cw = (cv + 7) & ~7;
+                        store16(stg, lane, w, hi, s.ld, rv, cw, 1);
+                        if (s.out2)
+                            store16(stg, lane, lw, static_cast<uint16_t *>(s.out2) + at, s.ld, rv,
+                                    cw, 1);
+                        if (s.sym && t.n0 + BN <= t.m0 && lane < rv) {
+                            // the mirrored place: a column is contiguous over the lanes
+                            const int64_t mt = (int64_t)t.g * s.out_group +
+                                               (int64_t)(t.n0 + c) * s.ld + m + lane;
+                            uint16_t *mh = static_cast<uint16_t *>(s.out) + mt;
+                            uint16_t *ml = static_cast<uint16_t *>(s.out2) + mt;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < cv) {
+                                    mh[(int64_t)i * s.ld] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                                    if (s.out2)
+                                        ml[(int64_t)i * s.ld] =
+                                            (uint16_t)(lw[i / 2] >> (16 * (i & 1)));
+                                }
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CTAS == 2)
+                    mbar_arrive_remote(map_to_rank(tempty_bar(slot), 0));
+                else
+                    mbar_arrive(tempty_bar(slot));
+            }
+        }
+    }
+
+    // ---- tear-down: all CTAs done with TMEM before it is freed ----
+    tc_fence_before();
+    __syncthreads();
+    if (CTAS == 2)
+        cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        if (CTAS == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(TMEM_COLS)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(TMEM_COLS)
+                         : "memory");
+    }
+}
+
+template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI>
+cudaError_t launch_one(const Params &p, cudaStream_t s)
+{
+    using S = Shape<CTAS, BN, EPI>;
+    static_assert(S::SMEM <= 232448, "shared memory");
+    static_assert(S::DH_COL + 2 * BN <= 512 || !S::ACT, "TMEM");
+    auto kern = grouped_kernel<CTAS, BN, A_MN, B_MN, EPI>;
+    cudaError_t err = raise_smem_limit((const void *)kern, S::SMEM);
+    if (err != cudaSuccess)
+        return err;
+    int units = device_sms();
+    if (CTAS == 2) {
+        err = cached_active_clusters((const void *)kern, THREADS, S::SMEM, 2, &units);
+        if (err != cudaSuccess)
+            return err;
+        if (units < 1)
+            return cudaErrorInvalidConfiguration;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(CTAS * units);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS == 2 ? 2 : 1;
+    err = cudaLaunchKernelEx(&cfg, kern, p);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+constexpr int kBnPair = 256, kBnOne = 128, kBnAct = 128;
+
+}  // namespace
+
+bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
+           int64_t groups, int64_t group_stride, int box_rows)
+{
+    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 64, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
+            int64_t groups, int64_t group_stride)
+{
+    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 64, 64,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int b_box_rows(Epi epi, bool pair)
+{
+    if (epi == EPI_SWIGLU)
+        return kBnAct;   // W1 and W3 boxes of BN rows each
+    if (epi == EPI_GELU)
+        return pair ? kBnAct / 2 : kBnAct;
+    return pair ? kBnPair / 2 : kBnOne;
+}
+
+cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t s)
+{
+    int ents = 0;
+    for (int i = 0; i < p.nsets; ++i) {
+        p.set[i].ent0 = ents;
+        ents += p.set[i].groups;
+    }
+    if (ents > kEntries)
+        return cudaErrorInvalidValue;
+    p.entries = ents;
+    p.timeout_ns = 2000000000ull;
+    switch (epi) {
+    case EPI_GELU:
+        return pair ? launch_one<2, kBnAct, false, false, EPI_GELU>(p, s)
+                    : launch_one<1, kBnAct, false, false, EPI_GELU>(p, s);
+    case EPI_SWIGLU:
+        return pair ? launch_one<2, kBnAct, false, false, EPI_SWIGLU>(p, s)
+                    : launch_one<1, kBnAct, false, false, EPI_SWIGLU>(p, s);
+    case EPI_DW:
+        return pair ? launch_one<2, kBnPair, true, true, EPI_DW>(p, s)
+                    : launch_one<1, kBnOne, true, true, EPI_DW>(p, s);
+    case EPI_ROWS:
+        if (layout == A_K_B_MN)
+            return pair ? launch_one<2, kBnPair, false, true, EPI_ROWS>(p, s)
+                        : launch_one<1, kBnOne, false, true, EPI_ROWS>(p, s);
+        return pair ? launch_one<2, kBnPair, false, false, EPI_ROWS>(p, s)
+                    : launch_one<1, kBnOne, false, false, EPI_ROWS>(p, s);
+    case EPI_NS:
+        if (layout == A_K_B_MN)
+            return pair ? launch_one<2, kBnPair, false, true, EPI_NS>(p, s)
+                        : launch_one<1, kBnOne, false, true, EPI_NS>(p, s);
+        if (layout == A_MN_B_MN)
+            return pair ? launch_one<2, kBnPair, true, true, EPI_NS>(p, s)
+                        : launch_one<1, kBnOne, true, true, EPI_NS>(p, s);
+        return pair ? launch_one<2, kBnPair, false, false, EPI_NS>(p, s)
+                    : launch_one<1, kBnOne, false, false, EPI_NS>(p, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace grp
+}  // namespace moe

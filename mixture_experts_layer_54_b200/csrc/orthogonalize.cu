@@ -1,0 +1,362 @@
+// Orthogonalised updates of stacked expert matrices by Newton-Schulz products:
+//   X = G / (|G|_F + eps), then `steps` times  A = X X^T (X^T X when X is
+//   tall), X = a X + (b A + c A A) X (a X + X (b A + c A A)),
+// which drives the singular values towards 1 and keeps the singular vectors.
+//
+// Bound by the tensor cores.  The products run on the fp16 pipe (the rate of
+// bf16, 3 more bits), on 2-byte copies of X, A and B = b A + c A A with fixed
+// powers of two as scales, so nothing is near the ends of fp16's range while
+// the singular values stay below about 2.8.  One rounding to fp16 (2^-11)
+// would be enough for a step on its own, but a step multiplies small singular
+// values by a = 3.4: noise that enters in the first of five steps comes out
+// 140 times as large against a low-rank gradient (1e-2 of the result, measured
+// in 64 bits).  So every step but the last holds X, A and B as two fp16 terms
+// (hi + lo, 22 bits) and computes hi hi + hi lo + lo hi in one fp32
+// accumulator; the last step's operands are single fp16, and the result is
+// within 1e-3 of the 64-bit one before its rounding to bf16.  A bf16 G times a
+// power of two is exact in one fp16 term.  A and B are symmetric: only tiles
+// on or below the diagonal are computed and mirrored.
+#include "grouped.cuh"
+
+#include <cuda_fp16.h>
+#include <math.h>
+#include <string.h>
+
+namespace moe {
+namespace grp {
+
+namespace {
+
+// stored value = true value times these
+constexpr float kSX = 8192.f, kSA = 8192.f, kSB = 2048.f;
+constexpr int kMaxParts = 64;
+
+inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// 8 consecutive elements from p (`vec`: p is 16-byte aligned), n of them valid
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int n, bool vec, float *f)
+{
+    if (vec && n >= 8) {
+        if (sizeof(T) == 2) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 u = reinterpret_cast<const float4 *>(p)[h];
+                f[4 * h] = u.x, f[4 * h + 1] = u.y, f[4 * h + 2] = u.z, f[4 * h + 3] = u.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = i < n ? to_f<T>(p[i]) : 0.f;
+    }
+}
+
+// Sums of squares of `parts` slices of each matrix (fp32 in a thread, then
+// double over the block; fixed order).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    square_sums_kernel(const T *G, int64_t mn, int parts, bool vec, double *out)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int e = blockIdx.y;
+    const T *g = G + e * mn;
+    float acc = 0.f;
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < mn; i += parts * 2048ll) {
+        float f[8];
+        load8(g + i, mn - i < 8 ? (int)(mn - i) : 8, vec, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc = fmaf(f[j], f[j], acc);
+    }
+    __shared__ double part[8];
+    double v = acc;
+#pragma unroll
+    for (int s = 16; s; s >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, s);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i)
+            v += part[i];
+        out[e * kMaxParts + blockIdx.x] = v;
+    }
+}
+
+// X = G 2^k as one or two fp16 terms, 2^k the power of two that brings |G| + eps
+// into (kSX / 2, kSX]; scale[e] = 2^k (|G| + eps) is then what X stands over.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    scale_kernel(const T *G, int m, int n, int64_t ld, int parts, bool vec, const double *sums,
+                 float eps, __half *hi, __half *lo, float *scale)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int e = blockIdx.y;
+    __shared__ float s_mul;
+    if (threadIdx.x == 0) {
+        double v = 0;
+        for (int i = 0; i < parts; ++i)
+            v += sums[e * kMaxParts + i];
+        const double norm = sqrt(v) + (double)eps;
+        int k = 0;
+        double mul = 1.0, sc = norm;   // zero with eps = 0: 0 / 0 as the formula has it
+        if (isfinite(norm) && norm > 0) {
+            k = 13 - (int)ceil(log2(norm));
+            k = min(max(k, -126), 126);
+            mul = exp2((double)k);
+            sc = mul * norm;
+        } else if (!isfinite(norm)) {
+            sc = nan("");   // an infinity or NaN in G: the whole update is NaN
+        }
+        s_mul = (float)mul;
+        if (blockIdx.x == 0)
+            scale[e] = (float)sc;
+    }
+    __syncthreads();
+    const float mul = s_mul;
+    const int cpr = (int)(ld / 8);
+    const int64_t chunks = (int64_t)m * cpr;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < chunks; i += gridDim.x * 256ll) {
+        const int64_t r = i / cpr;
+        const int c = (int)(i % cpr) * 8;
+        float f[8];
+        load8(G + ((int64_t)e * m + r) * n + c, n - c < 8 ? n - c : 8, vec, f);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x0 = f[2 * j] * mul, x1 = f[2 * j + 1] * mul;
+            const __half2 a = __floats2half2_rn(x0, x1);
+            const float2 b = __half22float2(a);
+            const __half2 d = __floats2half2_rn(x0 - b.x, x1 - b.y);
+            h[j] = *reinterpret_cast<const uint32_t *>(&a);
+            l[j] = *reinterpret_cast<const uint32_t *>(&d);
+        }
+        const int64_t o = ((int64_t)e * m + r) * ld + c;
+        *reinterpret_cast<uint4 *>(hi + o) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (lo)
+            *reinterpret_cast<uint4 *>(lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+struct Bufs {
+    int32_t *status;
+    double *sums;
+    float *scale;
+    __half *X[2][2], *A[2], *B[2];   // [ping-pong][hi, lo]
+    size_t bytes;
+};
+
+Bufs carve(int64_t E, int64_t m, int64_t n, int steps, void *ws)
+{
+    Bufs b;
+    char *base = static_cast<char *>(ws);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        void *p = base ? base + off : nullptr;
+        off = align_up(off + bytes, 256);
+        return p;
+    };
+    const int64_t p = m < n ? m : n;
+    const size_t x = (size_t)(E * m * up8(n)) * 2, a = (size_t)(E * p * up8(p)) * 2;
+    b.status = static_cast<int32_t *>(take(256));
+    b.sums = static_cast<double *>(take((size_t)E * kMaxParts * 8));
+    b.scale = static_cast<float *>(take((size_t)E * 4));
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            b.X[i][j] = static_cast<__half *>(take(steps > 1 || i + j == 0 ? x : 0));
+    for (int j = 0; j < 2; ++j) {
+        b.A[j] = static_cast<__half *>(take(steps > 1 || j == 0 ? a : 0));
+        b.B[j] = static_cast<__half *>(take(steps > 1 || j == 0 ? a : 0));
+    }
+    b.bytes = off;
+    return b;
+}
+
+}  // namespace
+
+size_t orthogonalize_bytes(int64_t E, int64_t m, int64_t n, int steps)
+{
+    return carve(E, m, n, steps, nullptr).bytes;
+}
+
+cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, int steps,
+                                 float a, float b, float c, float eps, float scale, void *U,
+                                 void *ws, cudaStream_t s)
+{
+    Bufs w = carve(E, m, n, steps, ws);
+    const int64_t mn = (int64_t)m * n, ldx = up8(n);
+    const bool wide = m <= n;
+    const int p = wide ? m : n, q = wide ? n : m;
+    const int64_t lda = up8(p);
+    const int esz = bf16 ? 2 : 4;
+    const bool al = (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
+    const int64_t want = ceil_div(mn, 256 * 8 * 4);
+    const int parts = (int)(want < 1 ? 1 : (want > kMaxParts ? kMaxParts : want));
+    const bool vsum = al && mn * esz % 16 == 0, vrow = al && (int64_t)n * esz % 16 == 0;
+    int64_t cblocks = ceil_div((int64_t)m * (ldx / 8), 256);
+    const int64_t most = ceil_div(148 * 16, E);
+    cblocks = cblocks > most ? most : cblocks;
+    // X0 needs its low half unless G is bf16 (exact in one term) or this is the only step
+    const bool lo0 = !bf16 && steps > 1;
+    cudaError_t err;
+    if (bf16) {
+        const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(G);
+        err = launch_pdl(square_sums_kernel<__nv_bfloat16>, dim3(parts, E), dim3(256), 0, s, g, mn,
+                         parts, vsum, w.sums);
+        if (err == cudaSuccess)
+            err = launch_pdl(scale_kernel<__nv_bfloat16>, dim3((unsigned)cblocks, E), dim3(256), 0,
+                             s, g, m, n, ldx, parts, vrow, (const double *)w.sums, eps, w.X[0][0],
+                             lo0 ? w.X[0][1] : nullptr, w.scale);
+    } else {
+        const float *g = static_cast<const float *>(G);
+        err = launch_pdl(square_sums_kernel<float>, dim3(parts, E), dim3(256), 0, s, g, mn, parts,
+                         vsum, w.sums);
+        if (err == cudaSuccess)
+            err = launch_pdl(scale_kernel<float>, dim3((unsigned)cblocks, E), dim3(256), 0, s, g, m,
+                             n, ldx, parts, vrow, (const double *)w.sums, eps, w.X[0][0],
+                             lo0 ? w.X[0][1] : nullptr, w.scale);
+    }
+    if (err != cudaSuccess)
+        return err;
+    const bool pair = p >= 256;
+    const int box = b_box_rows(EPI_NS, pair);
+    int cur = 0;
+    for (int i = 0; i < steps; ++i, cur ^= 1) {
+        const bool split = i + 1 < steps, last = i + 1 == steps;
+        const bool xlo = split && (i > 0 || lo0);
+        __half *const *X = w.X[cur];
+        const float xs = kSX;
+        bool ok = true;
+        Params P;
+        memset(&P, 0, sizeof P);
+        P.nsets = 1;
+        P.fp16 = 1;
+        P.status = w.status;
+        P.clear_status = i == 0;
+        Set &t = P.set[0];
+        t.mode = DENSE;
+        t.groups = E;
+        t.a_grouped = t.b_grouped = 1;
+
+        // A = X X^T (X^T X): hi hi + hi lo + lo hi
+        t.M = t.N = p;
+        t.K = q;
+        t.sym = 1;
+        t.segs = t.period = xlo ? 3 : 1;
+        t.seg_a = 4;
+        t.seg_b = 2;
+        for (int j = 0; j < (xlo ? 2 : 1); ++j) {
+            if (wide) {
+                ok &= map_k(&t.a[j], X[j], m, n, ldx, E, m * ldx, 128);
+                ok &= map_k(&t.b[j], X[j], m, n, ldx, E, m * ldx, box);
+            } else {
+                ok &= map_mn(&t.a[j], X[j], m, n, ldx, E, m * ldx);
+                t.b[j] = t.a[j];
+            }
+        }
+        t.out = w.A[0];
+        t.out2 = split ? w.A[1] : nullptr;
+        t.ld = (int)lda;
+        t.out_group = p * lda;
+        t.alpha = i == 0 ? kSA : kSA / (xs * xs);
+        t.scale = i == 0 ? w.scale : nullptr;
+        t.scale_pow = 2;
+        if (!ok)
+            return cudaErrorInvalidValue;
+        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_K : A_MN_B_MN, pair, s)) != cudaSuccess)
+            return err;
+
+        // B = b A + c A A
+        P.clear_status = 0;
+        t.K = p;
+        t.segs = t.period = split ? 3 : 1;
+        for (int j = 0; j < (split ? 2 : 1); ++j) {
+            ok &= map_k(&t.a[j], w.A[j], p, p, lda, E, p * lda, 128);
+            ok &= map_k(&t.b[j], w.A[j], p, p, lda, E, p * lda, box);
+        }
+        t.out = w.B[0];
+        t.out2 = split ? w.B[1] : nullptr;
+        t.alpha = c * kSB / (kSA * kSA);
+        t.beta = b * kSB / kSA;
+        t.base = w.A[0];
+        t.base2 = split ? w.A[1] : nullptr;
+        t.base_ld = (int)lda;
+        t.base_t = 1;
+        t.base_group = p * lda;
+        t.scale = nullptr;
+        if (!ok)
+            return cudaErrorInvalidValue;
+        if ((err = launch_tc(P, EPI_NS, A_K_B_K, pair, s)) != cudaSuccess)
+            return err;
+
+        // X = a X + B X (a X + X B)
+        t.sym = 0;
+        t.M = m;
+        t.N = n;
+        t.segs = t.period = split ? (xlo ? 3 : 2) : 1;
+        const int b_seg = 2, x_seg = 4;   // segment 1: low half of B; segment 2: of X
+        t.seg_a = wide ? b_seg : x_seg;
+        t.seg_b = wide ? x_seg : b_seg;
+        for (int j = 0; j < (split ? 2 : 1); ++j) {
+            if (wide) {
+                ok &= map_k(&t.a[j], w.B[j], p, p, lda, E, p * lda, 128);
+                if (j == 0 || xlo)
+                    ok &= map_mn(&t.b[j], X[j], m, n, ldx, E, m * ldx);
+            } else {
+                if (j == 0 || xlo)
+                    ok &= map_k(&t.a[j], X[j], m, n, ldx, E, m * ldx, 128);
+                ok &= map_k(&t.b[j], w.B[j], p, p, lda, E, p * lda, box);
+            }
+        }
+        const float mult = last ? scale : kSX;
+        t.alpha = i == 0 ? mult / kSB : mult / (kSB * xs);
+        t.beta = i == 0 ? a * mult : a * mult / xs;
+        t.scale = i == 0 ? w.scale : nullptr;
+        t.scale_pow = 1;
+        t.base = X[0];
+        t.base2 = xlo ? X[1] : nullptr;
+        t.base_ld = (int)ldx;
+        t.base_t = 0;
+        t.base_group = m * ldx;
+        if (last) {
+            t.out = U;
+            t.out2 = nullptr;
+            t.out_bf16 = 1;
+            t.ld = n;
+            t.out_group = mn;
+            t.vec = n % 8 == 0 && (reinterpret_cast<uintptr_t>(U) & 15u) == 0;
+        } else {
+            // the next step reads a low half unless it is the last
+            t.out = w.X[cur ^ 1][0];
+            t.out2 = i + 2 < steps ? w.X[cur ^ 1][1] : nullptr;
+            t.ld = (int)ldx;
+            t.out_group = m * ldx;
+        }
+        if (!ok)
+            return cudaErrorInvalidValue;
+        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_MN : A_K_B_K, pair, s)) != cudaSuccess)
+            return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace grp
+}  // namespace moe

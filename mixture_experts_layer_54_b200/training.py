@@ -1,0 +1,217 @@
+"""Binding of the expert training calls: the grouped products and their
+gradients, the gradients of the combine and of the expert FFNs, and the
+orthogonalised update.  Argument checks and marshalling only, as in ops.py;
+buffers that are not given are allocated with torch.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from ._abi import MoeConfig, check, lib
+from .ops import (DTYPE_BF16, DTYPE_F32, _p, _stream, _tdtype, moe_perm_rows, workspace)
+
+_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _code(t, what):
+    if t.dtype not in _CODES:
+        raise ValueError(f"{what} is {t.dtype}: fp32 or bf16 wanted")
+    return _CODES[t.dtype]
+
+
+def _is(t, shape, dtype, what):
+    """The library reads raw buffers: a wrong shape or type is refused here."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}: "
+                         f"{dtype} {tuple(shape)} wanted")
+
+
+def _grouped(a, W_shape, width, offsets, rows, what):
+    """(code, G, R, N, K) of a grouped product whose tall operand is a."""
+    if a.dim() != 2 or len(W_shape) != 3 or a.shape[1] != width:
+        raise ValueError(f"{what} {tuple(a.shape)} does not fit weights {tuple(W_shape)}")
+    G, N, K = W_shape
+    _is(offsets, (G + 1,), torch.int32, "offsets")
+    _is(rows, (G,), torch.int32, "rows")
+    return _code(a, what), int(G), int(a.shape[0]), int(N), int(K)
+
+
+def _ws(nbytes, ws, device):
+    return workspace(nbytes, device) if ws is None else ws
+
+
+def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
+    """y[r] = W[g] x[r] for the rows r of each group g: x [R, K], W [G, N, K],
+    offsets [G + 1] (and rows [G]) int32.  Rows of no group are not written."""
+    sizes = _grouped(x, W.shape, W.shape[-1], offsets, rows, "x")
+    _is(W, W.shape, x.dtype, "W")
+    shape = (x.shape[0], W.shape[1])
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    _is(y, shape, x.dtype, "y")
+    ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, x.device)
+    check(lib().moe_grouped_matmul(*sizes, _p(x), _p(W), _p(offsets), _p(rows), _p(y), _p(ws),
+                                   ws.numel(), _stream()), "moe_grouped_matmul")
+    return y
+
+
+def moe_grouped_matmul_dx(dy, W, offsets, rows=None, dx=None, ws=None):
+    """Gradient of moe_grouped_matmul by x: dx[r] = W[g]^T dy[r], dy [R, N]."""
+    sizes = _grouped(dy, W.shape, W.shape[-2], offsets, rows, "dy")
+    _is(W, W.shape, dy.dtype, "W")
+    shape = (dy.shape[0], W.shape[2])
+    if dx is None:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+    _is(dx, shape, dy.dtype, "dx")
+    ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, dy.device)
+    check(lib().moe_grouped_matmul_dx(*sizes, _p(dy), _p(W), _p(offsets), _p(rows), _p(dx), _p(ws),
+                                      ws.numel(), _stream()), "moe_grouped_matmul_dx")
+    return dx
+
+
+def moe_grouped_matmul_dw(dy, x, offsets, rows=None, add=None, dW=None, out_dtype=None, ws=None):
+    """Gradient of moe_grouped_matmul by W: dW[g] = (add[g] +) sum of dy[r] x[r]^T
+    over the rows r of group g.  dW may be add itself (summing over
+    micro-batches); out_dtype defaults to that of add, dW or dy."""
+    G = offsets.shape[0] - 1
+    if dy.dim() != 2 or x.dim() != 2:
+        raise ValueError("dy and x are [R, N] and [R, K]")
+    shape = (G, dy.shape[1], x.shape[1])
+    sizes = _grouped(dy, shape, shape[1], offsets, rows, "dy")
+    _is(x, (dy.shape[0], shape[2]), dy.dtype, "x")
+    if out_dtype is None:
+        out_dtype = next((t.dtype for t in (add, dW) if t is not None), dy.dtype)
+    if dW is None:
+        dW = torch.empty(shape, dtype=out_dtype, device=dy.device)
+    _is(dW, shape, out_dtype, "dW")
+    _is(add, shape, out_dtype, "add")
+    ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, dy.device)
+    check(lib().moe_grouped_matmul_dw(*sizes, _p(dy), _p(x), _p(offsets), _p(rows),
+                                      _code(dW, "dW"), _p(add), _p(dW), _p(ws), ws.numel(),
+                                      _stream()), "moe_grouped_matmul_dw")
+    return dW
+
+
+def moe_combine_backward(cfg: MoeConfig, dy, Y_perm, gates, topk, pos, keep, offsets, dY_perm=None,
+                         dgates=None):
+    """Gradients of moe_combine: (dY_perm, dgates).  Padding rows of dY_perm are
+    not written."""
+    T, k, d, dt = cfg.T, cfg.k, cfg.d, _tdtype(cfg)
+    R = moe_perm_rows(cfg)
+    if dY_perm is None:
+        dY_perm = torch.empty((R, d), dtype=dt, device=dy.device)
+    if dgates is None:
+        dgates = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    for t, shape, dtype, what in ((dy, (T, d), dt, "dy"), (Y_perm, (R, d), dt, "Y_perm"),
+                                  (dY_perm, (R, d), dt, "dY_perm"),
+                                  (gates, (T, k), torch.float32, "gates"),
+                                  (dgates, (T, k), torch.float32, "dgates"),
+                                  (topk, (T, k), torch.int32, "topk"),
+                                  (pos, (T, k), torch.int32, "pos"),
+                                  (keep, (T, k), torch.uint8, "keep"),
+                                  (offsets, (cfg.E + 1,), torch.int32, "offsets")):
+        _is(t, shape, dtype, what)
+    check(lib().moe_combine_backward(ctypes.byref(cfg), _p(dy), _p(Y_perm), _p(gates), _p(topk),
+                                     _p(pos), _p(keep), _p(offsets), _p(dY_perm), _p(dgates),
+                                     _stream()), "moe_combine_backward")
+    return dY_perm, dgates
+
+
+def moe_ffn_backward_workspace_size(cfg: MoeConfig) -> int:
+    return int(lib().moe_ffn_backward_workspace_size(ctypes.byref(cfg)))
+
+
+@dataclass
+class FFNGrads:
+    """Gradients of moe_expert_ffn's inputs (None where the layer has none)."""
+    dx_perm: torch.Tensor
+    dW1: torch.Tensor
+    dW3: torch.Tensor | None
+    dW2: torch.Tensor
+    dx_shared: torch.Tensor | None = None
+    dWs1: torch.Tensor | None = None
+    dWs3: torch.Tensor | None = None
+    dWs2: torch.Tensor | None = None
+
+
+def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, W3, W2, x=None,
+                            dY_shared=None, Ws1=None, Ws3=None, Ws2=None, dx_perm=None,
+                            grads: FFNGrads | None = None, dw_dtype=None, accumulate=False,
+                            ws=None) -> FFNGrads:
+    """Gradients of moe_expert_ffn, the hidden activations computed again from
+    x_perm (and x for the shared experts).  kept [E] are the capacity stage's row
+    counts.  `grads` gives the output buffers (dx_perm alone its own); with
+    accumulate the weight gradients are added to what they hold."""
+    E, d, F, T, S, Fs = cfg.E, cfg.d, cfg.d_ff, cfg.T, cfg.n_shared, cfg.d_ff_shared
+    dt, dev = _tdtype(cfg), x_perm.device
+    R = moe_perm_rows(cfg)
+    swiglu = cfg.act == 1
+    if accumulate and grads is None:
+        raise ValueError("accumulate adds to the weight gradients in `grads`")
+    if grads is None:
+        wt = dt if dw_dtype is None else dw_dtype
+        e = lambda *shape, t=wt: torch.empty(shape, dtype=t, device=dev)
+        grads = FFNGrads(dx_perm=e(R, d, t=dt) if dx_perm is None else dx_perm, dW1=e(E, F, d),
+                         dW3=e(E, F, d) if swiglu else None, dW2=e(E, d, F))
+        if S:
+            grads.dx_shared = e(T, d, t=dt)
+            grads.dWs1, grads.dWs2 = e(S, Fs, d), e(S, d, Fs)
+            grads.dWs3 = e(S, Fs, d) if swiglu else None
+    elif dx_perm is not None:
+        grads.dx_perm = dx_perm
+    g = grads
+    wt = g.dW1.dtype
+    if dw_dtype is not None and dw_dtype != wt:
+        raise ValueError(f"dw_dtype {dw_dtype} but dW1 is {wt}")
+    for t, shape, dtype, what in (
+            (x_perm, (R, d), dt, "x_perm"), (dY_perm, (R, d), dt, "dY_perm"),
+            (offsets, (E + 1,), torch.int32, "offsets"), (kept, (E,), torch.int32, "kept"),
+            (W1, (E, F, d), dt, "W1"), (W3, (E, F, d), dt, "W3"), (W2, (E, d, F), dt, "W2"),
+            (x, (T, d), dt, "x"), (dY_shared, (T, d), dt, "dY_shared"),
+            (Ws1, (S, Fs, d), dt, "Ws1"), (Ws3, (S, Fs, d), dt, "Ws3"),
+            (Ws2, (S, d, Fs), dt, "Ws2"), (g.dx_perm, (R, d), dt, "dx_perm"),
+            (g.dW1, (E, F, d), wt, "dW1"), (g.dW3, (E, F, d), wt, "dW3"),
+            (g.dW2, (E, d, F), wt, "dW2"), (g.dx_shared, (T, d), dt, "dx_shared"),
+            (g.dWs1, (S, Fs, d), wt, "dWs1"), (g.dWs3, (S, Fs, d), wt, "dWs3"),
+            (g.dWs2, (S, d, Fs), wt, "dWs2")):
+        _is(t, shape, dtype, what)
+    ws = _ws(moe_ffn_backward_workspace_size(cfg), ws, dev)
+    check(lib().moe_expert_ffn_backward(
+        ctypes.byref(cfg), _p(x_perm), _p(offsets), _p(kept), _p(dY_perm), _p(W1), _p(W3), _p(W2),
+        _p(x), _p(dY_shared), _p(Ws1), _p(Ws3), _p(Ws2), _p(g.dx_perm), _p(g.dW1), _p(g.dW3),
+        _p(g.dW2), _p(g.dx_shared), _p(g.dWs1), _p(g.dWs3), _p(g.dWs2), _code(g.dW1, "dW1"),
+        int(bool(accumulate)), _p(ws), ws.numel(), _stream()), "moe_expert_ffn_backward")
+    return grads
+
+
+def moe_orthogonalize_workspace_size(E: int, m: int, n: int, steps: int = 5) -> int:
+    return int(lib().moe_orthogonalize_workspace_size(int(E), int(m), int(n), int(steps)))
+
+
+def moe_orthogonalize(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), scale=1.0, eps=1e-7, U=None,
+                      ws=None):
+    """Every update G[e] ([E, m, n], or one [m, n]; fp32 or bf16) with its
+    singular values driven towards 1 by `steps` Newton-Schulz steps, times scale,
+    as bf16."""
+    if G.dim() not in (2, 3):
+        raise ValueError(f"G is {tuple(G.shape)}: [E, m, n] or [m, n] wanted")
+    E, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
+    if U is None:
+        U = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+    _is(U, G.shape, torch.bfloat16, "U")
+    c = (ctypes.c_float * 3)(*coeffs)
+    ws = _ws(moe_orthogonalize_workspace_size(E, m, n, steps), ws, G.device)
+    check(lib().moe_orthogonalize(_code(G, "G"), E, m, n, _p(G), int(steps), c, float(eps),
+                                  float(scale), _p(U), _p(ws), ws.numel(), _stream()),
+          "moe_orthogonalize")
+    return U
+
+
+__all__ = ["moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
+           "moe_combine_backward", "moe_expert_ffn_backward", "moe_ffn_backward_workspace_size",
+           "FFNGrads", "moe_orthogonalize", "moe_orthogonalize_workspace_size"]
