@@ -256,8 +256,10 @@ def _run_own(s, case):
     if op == "combine_grad":
         cfg = moe.moe_config(T=case["T"], d=case["d"], E=case["E"], k=case["k"], d_ff=64, act=1,
                              dtype=int(case["dtype"] == "bf16"), cf=_cf(case))
-        return moe.moe_combine_backward(cfg, s["dy"], s["Y_perm"], s["gates"], s["topk"], s["pos"],
-                                        s["keep"], s["offsets"], dY_perm=s["dY_perm"])
+        dY_perm, dgates = moe.moe_combine_backward(cfg, s["dy"], s["Y_perm"], s["gates"], s["topk"],
+                                                   s["pos"], s["keep"], s["offsets"],
+                                                   dY_perm=s["dY_perm"])
+        return {"dY_perm": dY_perm, "dgates": dgates}
     if op == "ffn_grad":
         cfg = moe.moe_config(T=case["T"], d=case["d"], E=case["E"], k=case["k"], d_ff=case["d_ff"],
                              n_shared=case["n_shared"], d_ff_shared=case["d_ff_shared"],
