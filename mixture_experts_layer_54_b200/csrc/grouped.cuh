@@ -43,12 +43,12 @@ struct Set {
     float alpha, beta;
     const float *scale;          // nullable: scale[g] divides as scale_pow says
     int scale_pow;               // val = alpha / s^pow acc + beta / s base (s once for pow < 2)
-    int vec;                     // 1: 16-byte rows (out aligned, ld a multiple of 8)
+    int bytes;                   // alignment of the output rows (32, 16 or 2), found at launch
 };
 
 struct __align__(64) Params {
     Set set[kSets];
-    int nsets, entries;
+    int nsets, entries;          // set 0 is the ragged one, if any is
     const int32_t *offsets;      // [G + 1]
     const int32_t *rows;         // [G], nullable: offsets[g + 1] - offsets[g]
     int n_rows;                  // rows of the tall buffers; the table is held inside them

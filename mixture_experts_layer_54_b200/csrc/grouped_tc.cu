@@ -17,13 +17,18 @@
 // row; the producer waits for that box and clears the up to 15 rows behind it
 // in shared memory before handing the stage over.
 //
-// Output rows go through a 2 KB staging tile per epilogue warp to 64-byte
-// pieces of rows, each masked by the group's end: rows behind it are neither
-// written nor read.
+// The tensor cores truncate when they add to an fp32 accumulator, a bias of
+// about 2e-8 of the sum for every 16 rows (measured: 1.6e-6 after 1536 rows,
+// where fp32 rounding alone leaves 3e-7), so a weight gradient over many rows
+// is summed in accumulators of 512 rows each, which the epilogue adds up in
+// registers (round to nearest) while the next one fills: 128 values a thread.
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs (and owns TMEM), warps 2..9 are
-// the epilogue (warp w reads TMEM lanes 32 (w mod 4) .. +31, warps 2..5 the
-// first half of the columns).  Every wait is bounded; on expiry the CTA sets
+// Output rows go from registers to memory, each masked by the group's end: rows
+// behind it are neither written nor read.
+//
+// Roles: warp 0 loads, warp 1 issues the MMAs (and owns TMEM), the last eight
+// are the epilogue (warp w reads TMEM lanes 32 (w mod 4) .. +31, the first four
+// of them the first half of the columns).  Every wait is bounded; on expiry the CTA sets
 // MOE_ERR_DEVICE_TIMEOUT, every role leaves its loop, copies in flight are
 // awaited (bounded too), TMEM is freed and the kernel returns.
 #include "grouped.cuh"
@@ -39,9 +44,7 @@ using namespace tc;
 namespace {
 
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int A_BYTES = 128 * 128;       // 128 rows x 64 elements of one CTA
-constexpr int STG_WARP = 32 * 64;        // staging tile of an epilogue warp: 32 rows x 64 bytes
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int RING_BYTES = 192 * 1024;
 
@@ -49,6 +52,8 @@ template <int CTAS, int BN, int EPI>
 struct Shape {
     static constexpr bool ACT = EPI == EPI_GELU || EPI == EPI_SWIGLU;
     static constexpr int BM = 128 * CTAS;
+    static constexpr int FIRST_EPI = 2;   // first of the epilogue warps
+    static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
     // accumulator columns of the widest B tile (ACT: u, with v beside it)
     static constexpr int BNB = EPI == EPI_SWIGLU ? 2 * BN : BN;
     static constexpr int B_ROWS = BNB / CTAS;            // B rows of one CTA
@@ -59,10 +64,12 @@ struct Shape {
     static constexpr int STAGES = RING_BYTES / (KSUB * SUB) > 6 ? 6 : RING_BYTES / (KSUB * SUB);
     static constexpr int BK = 64 * KSUB;
     static constexpr int OFF_B = STAGES * KSUB * A_BYTES;
-    static constexpr int OFF_STG = OFF_B + STAGES * KSUB * B_BYTES;
-    static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * STG_WARP;
+    static constexpr int OFF_BAR = OFF_B + STAGES * KSUB * B_BYTES;
     static constexpr int OFF_TAB = OFF_BAR + 256;
-    static constexpr int SMEM = OFF_TAB + 4 * (kEntries + 1) + 1024;   // + alignment slack
+    static constexpr int SMEM = OFF_TAB + 4 * (kEntries + 1) + 8 * kMaxE + 1024;   // + alignment slack
+    // EPI_DW: contraction rows summed in one accumulator before the epilogue
+    // adds it, in registers, to the tile's running sum (0: all of them)
+    static constexpr int CHUNK = EPI == EPI_DW ? 512 : 0;
     // TMEM columns.  Plain: two accumulators of BN.  GELU: u and dh, twice.
     // SwiGLU: u | v once (256 columns), dh twice behind it.
     static constexpr int DH_COL = EPI == EPI_SWIGLU ? 2 * BN : BN;
@@ -78,13 +85,9 @@ struct Tile {
 
 // Tiles of entry (set, g).
 template <int BM, int BN>
-__device__ __forceinline__ int entry_tiles(const Params &p, const Set &s, int g)
+__device__ __forceinline__ int entry_tiles(const Set &s, const int2 *span, int g)
 {
-    int m = s.M;
-    if (s.mode == RAGGED_M) {
-        int start;
-        group_rows(p.offsets, p.rows, p.n_rows, g, &start, &m);
-    }
+    const int m = s.mode == RAGGED_M ? span[g].y : s.M;
     const int mt = (m + BM - 1) / BM, nt = (s.N + BN - 1) / BN;
     if (!s.sym)
         return mt * nt;
@@ -95,7 +98,7 @@ __device__ __forceinline__ int entry_tiles(const Params &p, const Set &s, int g)
 }
 
 template <int BM, int BN>
-__device__ __forceinline__ Tile decode(const Params &p, const int *tstart, int tile)
+__device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const int2 *span, int tile)
 {
     int lo = 0, hi = p.entries;   // last entry with tstart <= tile
     while (hi - lo > 1) {
@@ -117,9 +120,9 @@ __device__ __forceinline__ Tile decode(const Params &p, const int *tstart, int t
     t.k0 = 0;
     t.klen = s.K;
     if (s.mode == RAGGED_M)
-        group_rows(p.offsets, p.rows, p.n_rows, t.g, &t.row0, &t.mg);
+        t.row0 = span[t.g].x, t.mg = span[t.g].y;
     else if (s.mode == RAGGED_K)
-        group_rows(p.offsets, p.rows, p.n_rows, t.g, &t.k0, &t.klen);
+        t.k0 = span[t.g].x, t.klen = span[t.g].y;
     int i = tile - tstart[lo];
     const int nt = (s.N + BN - 1) / BN;
     if (s.sym) {
@@ -188,12 +191,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
         tma_load_3d(dst, m, bar, c0, c1, c2);
 }
 
-// arrive (with `bytes` more to come, if any) on the leader's barrier
+// Arrive on the leader's barrier with `bytes` to come by TMA.  Nothing this
+// thread wrote has to be seen by the waiter, so the arrival is relaxed (a
+// release at cluster scope for every stage doubled the kernel's time).
 template <int CTAS>
-__device__ __forceinline__ void arrive_leader(uint32_t bar, uint32_t bytes)
+__device__ __forceinline__ void arrive_bytes(uint32_t bar, uint32_t bytes)
 {
     if (CTAS == 2)
-        asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::
                          "r"(bar),
                      "r"(bytes)
                      : "memory");
@@ -201,70 +206,95 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar, uint32_t bytes)
         mbar_expect_tx(bar, bytes);
 }
 
-// 32 columns of packed 16-bit values of this lane's row -> rows of the output.
-// dst: row 0, column 0 of the piece; rv rows and cv columns of it are stored.
-__device__ __forceinline__ void store16(uint8_t *stg, int lane, const uint32_t *packed,
-                                        uint16_t *dst, int64_t ld, int rv, int cv, int vec)
+// Arrive on the leader's barrier after this warp's own writes to the stage.
+template <int CTAS>
+__device__ __forceinline__ void arrive_written(uint32_t bar)
 {
-    __syncwarp();
+    if (CTAS == 2)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                     : "memory");
+    else
+        mbar_arrive(bar);
+}
+
+// Every lane stores its own row, 32 bytes at a time where the rows start on
+// 32-byte boundaries (whole sectors; a warp's 32 rows through a staging tile in
+// shared memory to 64-byte pieces measured 3 times as long), else 16.
+__device__ __forceinline__ void st32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st16(void *p, const uint32_t *w)
+{
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 32 columns of packed 16-bit values of this lane's row, the first cv of them
+// (a multiple of 8 unless bytes is 2) to dst.  bytes: what every row is aligned to.
+__device__ __forceinline__ void store16(const uint32_t *w, uint16_t *dst, int cv, int bytes)
+{
+    if (bytes == 32) {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(packed[4 * ch], packed[4 * ch + 1], packed[4 * ch + 2],
-                       packed[4 * ch + 3]);
-    __syncwarp();
-    if (vec) {
-        const int ch = lane & 3;
+        for (int c = 0; c < 2; ++c)
+            if (16 * c < cv)
+                st32(dst + 16 * c, w + 8 * c);
+    } else if (bytes == 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (lane >> 2) + 8 * i;
-            if (r < rv && ch * 8 < cv)
-                *reinterpret_cast<uint4 *>(dst + r * ld + ch * 8) =
-                    *reinterpret_cast<const uint4 *>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-        }
+        for (int c = 0; c < 4; ++c)
+            if (8 * c < cv)
+                st16(dst + 8 * c, w + 4 * c);
     } else {
-        for (int r = 0; r < min(rv, 32); ++r)
-            if (lane < cv)
-                dst[r * ld + lane] = *reinterpret_cast<const uint16_t *>(
-                    stg + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (c < cv)
+                dst[c] = (uint16_t)(w[c / 2] >> (16 * (c & 1)));
     }
 }
 
-// 16 fp32 columns of this lane's row, plus the addend, to fp32 or bf16 rows.
-__device__ __forceinline__ void store_dw(uint8_t *stg, int lane, const float *v, const Set &s,
-                                         int64_t at, int rv, int cv)
+__device__ __forceinline__ void ld32(const void *p, uint32_t *w)
 {
-    __syncwarp();
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// n 32-byte pieces of a row, those that begin before byte `end`
+template <int N>
+__device__ __forceinline__ void load_row(const uint8_t *p, int end, int bytes, uint32_t *w)
+{
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-        *reinterpret_cast<float4 *>(stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
-            make_float4(v[4 * ch], v[4 * ch + 1], v[4 * ch + 2], v[4 * ch + 3]);
-    __syncwarp();
-    const int ch = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (lane >> 2) + 8 * i;
-        if (r >= rv || ch * 4 >= cv)
-            continue;
-        float4 f = *reinterpret_cast<const float4 *>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-        const int64_t o = at + (int64_t)r * s.ld + ch * 4;
-        if (s.out_f32) {
-            if (s.add) {
-                const float4 a = *reinterpret_cast<const float4 *>(
-                    static_cast<const float *>(s.add) + o);
-                f.x += a.x, f.y += a.y, f.z += a.z, f.w += a.w;
-            }
-            *reinterpret_cast<float4 *>(static_cast<float *>(s.out) + o) = f;
+    for (int c = 0; c < N; ++c) {
+        if (bytes == 32) {
+            if (32 * c < end)
+                ld32(p + 32 * c, w + 8 * c);
         } else {
-            if (s.add) {
-                const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162 *>(
-                    static_cast<const __nv_bfloat16 *>(s.add) + o);
-                const float2 a0 = __bfloat1622float2(a[0]), a1 = __bfloat1622float2(a[1]);
-                f.x += a0.x, f.y += a0.y, f.z += a1.x, f.w += a1.y;
-            }
-            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(f.x, f.y), __floats2bfloat162_rn(f.z, f.w)};
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(s.out) + o) =
-                *reinterpret_cast<uint2 *>(h);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (32 * c + 16 * h < end) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(p + 32 * c + 16 * h);
+                    w[8 * c + 4 * h] = u.x, w[8 * c + 4 * h + 1] = u.y;
+                    w[8 * c + 4 * h + 2] = u.z, w[8 * c + 4 * h + 3] = u.w;
+                }
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_row(uint8_t *p, int end, int bytes, const uint32_t *w)
+{
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        if (bytes == 32) {
+            if (32 * c < end)
+                st32(p + 32 * c, w + 8 * c);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (32 * c + 16 * h < end)
+                    st16(p + 32 * c + 16 * h, w + 8 * c + 4 * h);
         }
     }
 }
@@ -288,12 +318,12 @@ __device__ __forceinline__ float2 unpack_fp16(uint32_t u)
 // the (symmetric) base at the transposed place, where a column is contiguous
 // over the warp's rows.
 __device__ __forceinline__ void ns_values(const Set &s, int g, float alpha, float beta, int row,
-                                          int col, int rv, int cv, int lane, float *v)
+                                          int col, bool mine, int cv, float *v)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         v[i] *= alpha;
-    if (!s.base || lane >= rv)
+    if (!s.base || !mine)
         return;
     const int64_t g0 = (int64_t)g * s.base_group;
     const __half *hi = static_cast<const __half *>(s.base) + g0;
@@ -339,7 +369,8 @@ __device__ __forceinline__ void ns_values(const Set &s, int g, float alpha, floa
 }
 
 template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
+    grouped_kernel(const __grid_constant__ Params p)
 {
     using S = Shape<CTAS, BN, EPI>;
     constexpr bool ACT = S::ACT;
@@ -358,7 +389,8 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     const uint32_t tail_bar = bar0 + 8u * (2 * STAGES + 5);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + 8 * (2 * STAGES + 6));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *tstart = reinterpret_cast<int *>(smem + S::OFF_TAB);   // [entries + 1]
+    int2 *span = reinterpret_cast<int2 *>(smem + S::OFF_TAB);   // [groups] first row, rows
+    int *tstart = reinterpret_cast<int *>(span + kMaxE);        // [entries + 1]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
@@ -400,7 +432,11 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0)
         *p.status = 0;
     if (warp == 2) {
-        // tile table: running sum of the entries' tiles
+        // the segment table, and the tile table: running sum of the entries' tiles
+        if (p.set[0].mode != DENSE)
+            for (int g = lane; g < p.set[0].groups; g += 32)
+                group_rows(p.offsets, p.rows, p.n_rows, g, &span[g].x, &span[g].y);
+        __syncwarp();
         int base = 0;
         for (int e0 = 0; e0 < p.entries; e0 += 32) {
             const int e = e0 + lane;
@@ -409,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                 int set = 0;
                 while (set + 1 < p.nsets && p.set[set + 1].ent0 <= e)
                     ++set;
-                n = entry_tiles<BM, BN>(p, p.set[set], e - p.set[set].ent0);
+                n = entry_tiles<BM, BN>(p.set[set], span, e - p.set[set].ent0);
             }
             int sum = n;
 #pragma unroll
@@ -442,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         uint32_t last_phase = 0;   // bit s: phase of stage s's last use
         bool ok = true;
         for (int tile = unit; ok && tile < total; tile += units) {
-            const Tile t = decode<BM, BN>(p, tstart, tile);
+            const Tile t = decode<BM, BN>(p, tstart, span, tile);
             const Set &s = p.set[t.set];
             const int m_row = t.m0 + (int)rank * 128 + (s.mode == RAGGED_M ? t.row0 : 0);
             const int segs = ACT ? 2 : s.segs;
@@ -476,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                         if (tail)
                             mbar_expect_tx(tail_bar, bytes);
                         else
-                            arrive_leader<CTAS>(fb, bytes);
+                            arrive_bytes<CTAS>(fb, bytes);
                         for (int ks = 0; ks < nks; ++ks) {
                             const int kc = t.k0 + kb * S::BK + ks * 64;
                             const uint32_t da = sA + (stage * KSUB + ks) * A_BYTES;
@@ -525,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0)
-                            arrive_leader<CTAS>(fb, 0);
+                            arrive_written<CTAS>(fb);
                         if (!okw) {
                             ok = false;
                             break;
@@ -555,9 +591,9 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
             int it = 0;
             bool ok = true, any = false;
             for (int tile = unit; ok && tile < total; tile += units, ++it) {
-                const Tile t = decode<BM, BN>(p, tstart, tile);
+                const Tile t = decode<BM, BN>(p, tstart, span, tile);
                 const Set &s = p.set[t.set];
-                const int slot = it & 1;
+                int slot = it & 1;
                 if (!wait_bar(tempty_bar(slot), ((it >> 1) & 1) ^ 1u, ctl)) {
                     ok = false;
                     break;
@@ -589,12 +625,29 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                                            (b_mn ? 1u << 16 : 0u) |
                                            ((uint32_t)((uv ? 2 * BN : BN) >> 3) << 17);
                     for (int kb = 0; kb * S::BK < t.klen; ++kb) {
-                        if (!wait_bar<true>(full_bar(stage), phase, ctl)) {
+                        if (S::CHUNK > 0 && kb > 0 && kb % (S::CHUNK > 0 ? S::CHUNK / S::BK : 1) == 0) {
+                            // this accumulator is full: on to the other one
+                            commit_all<CTAS>(tfull_bar(slot));
+                            ++it;
+                            slot = it & 1;
+                            d = tmem_base + slot * BN;
+                            first = true;
+                            if (!wait_bar(tempty_bar(slot), ((it >> 1) & 1) ^ 1u, ctl)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        const int rem = t.klen - kb * S::BK;
+                        // a cleared tail: the other CTA's threads wrote to the stage too
+                        const bool got = A_MN && rem < S::BK
+                                             ? wait_bar<true>(full_bar(stage), phase, ctl)
+                                             : wait_bar(full_bar(stage), phase, ctl);
+                        if (!got) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const int rem = t.klen - kb * S::BK;
                         const int steps = rem >= S::BK ? S::BK / 16 : (rem + 15) / 16;
 #pragma unroll
                         for (int st = 0; st < S::BK / 16; ++st) {
@@ -629,15 +682,14 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                 wait_bar(drain_bar, 0, ctl, false);
             }
         }
-    } else {
-        // ================= epilogue (warps 2..9, both CTAs) =================
-        const int q = warp & 3, ew = warp - 2, half = ew >> 2;
-        uint8_t *stg = smem + S::OFF_STG + ew * STG_WARP;
+    } else if (warp >= S::FIRST_EPI) {
+        // ================= epilogue (eight warps, both CTAs) =================
+        const int q = warp & 3, half = (warp - S::FIRST_EPI) >> 2;
         int it = 0;
         for (int tile = unit; tile < total; tile += units, ++it) {
-            const Tile t = decode<BM, BN>(p, tstart, tile);
+            const Tile t = decode<BM, BN>(p, tstart, span, tile);
             const Set &s = p.set[t.set];
-            const int slot = it & 1;
+            int slot = it & 1;
             if (!wait_bar(tfull_bar(slot), (it >> 1) & 1, ctl))
                 break;
             tc_fence_after();
@@ -645,9 +697,101 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
             const int m = t.m0 + (int)rank * 128 + q * 32;   // first row, in the group
             const int rv = t.mg - m;                          // rows of it from there on
             const int c_end = rv > 0 ? min((half + 1) * (BN / 2), s.N - t.n0) : 0;
-            const int64_t row = m + (s.mode == RAGGED_M ? t.row0 : 0);
+            const int64_t row = m + lane + (s.mode == RAGGED_M ? t.row0 : 0);
             const int64_t at0 = (s.mode == RAGGED_M ? 0 : (int64_t)t.g * s.out_group) +
                                 row * s.ld + t.n0;
+            const bool mine = lane < rv;
+            const int bytes = s.bytes;
+            if constexpr (EPI == EPI_DW) {
+                float sum[BN / 2];
+                if (t.klen == 0) {   // nothing was accumulated: an empty group's sum
+#pragma unroll
+                    for (int i = 0; i < BN / 2; ++i)
+                        sum[i] = 0.f;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < BN / 64; ++i)
+                        tmem_ld32(tq + slot * BN + half * (BN / 2) + 32 * i, sum + 32 * i);
+                }
+                bool ok = true;
+                for (int k = S::CHUNK; k < t.klen; k += S::CHUNK) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CTAS == 2)
+                            mbar_arrive_remote(map_to_rank(tempty_bar(slot), 0));
+                        else
+                            mbar_arrive(tempty_bar(slot));
+                    }
+                    ++it;
+                    slot = it & 1;
+                    if (!wait_bar(tfull_bar(slot), (it >> 1) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i) {
+                        float v[16];
+                        tmem_ld16(tq + slot * BN + half * (BN / 2) + 16 * i, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[16 * i + j] += v[j];
+                    }
+                }
+                if (!ok)
+                    break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {   // the sums are in registers: release TMEM before the stores
+                    if (CTAS == 2)
+                        mbar_arrive_remote(map_to_rank(tempty_bar(slot), 0));
+                    else
+                        mbar_arrive(tempty_bar(slot));
+                }
+                if (mine) {
+                    const int c0 = half * (BN / 2), cols = c_end - c0;
+                    const int esz = s.out_f32 ? 4 : 2;
+                    uint8_t *out = static_cast<uint8_t *>(s.out) + (at0 + c0) * esz;
+                    const uint8_t *add = s.add ? static_cast<const uint8_t *>(s.add) +
+                                                     (at0 + c0) * esz
+                                               : nullptr;
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i) {   // 16 columns at a time
+                        float *v = sum + 16 * i;
+                        const int end = (cols - 16 * i) * esz;
+                        uint32_t w[16];
+                        if (s.out_f32) {
+                            if (add) {
+                                load_row<2>(add + 64 * i, end, bytes, w);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    w[j] = __float_as_uint(v[j] + __uint_as_float(w[j]));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    w[j] = __float_as_uint(v[j]);
+                            }
+                            store_row<2>(out + 64 * i, end, bytes, w);
+                        } else {
+                            if (add) {
+                                load_row<1>(add + 32 * i, end, bytes, w);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    w[j] = pack_bf16(v[2 * j] + __uint_as_float(w[j] << 16),
+                                                     v[2 * j + 1] +
+                                                         __uint_as_float(w[j] & 0xffff0000u));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                            }
+                            store_row<1>(out + 32 * i, end, bytes, w);
+                        }
+                    }
+                }
+                continue;
+            }
 #pragma unroll 1
             for (int c = half * (BN / 2); c < c_end; c += 32) {
                 const int cv = s.N - t.n0 - c;
@@ -681,8 +825,10 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                             w[i / 2] = pack_bf16(h[0], h[1]);
                             g[i / 2] = pack_bf16(du[0], du[1]);
                         }
-                        store16(stg, lane, w, static_cast<uint16_t *>(s.out) + at, s.ld, rv, cv, 1);
-                        store16(stg, lane, g, static_cast<uint16_t *>(s.out2) + at, s.ld, rv, cv, 1);
+                        if (mine) {
+                            store16(w, static_cast<uint16_t *>(s.out) + at, cv, bytes);
+                            store16(g, static_cast<uint16_t *>(s.out2) + at, cv, bytes);
+                        }
                     } else {
                         float x3[32];
                         tmem_ld32(tu + BN, x3);
@@ -703,39 +849,35 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                             g[i / 2] = pack_bf16(du[0], du[1]);
                             k[i / 2] = pack_bf16(dv[0], dv[1]);
                         }
-                        store16(stg, lane, w, static_cast<uint16_t *>(s.out) + at, s.ld, rv, cv, 1);
-                        store16(stg, lane, g, static_cast<uint16_t *>(s.out2) + at, s.ld, rv, cv, 1);
-                        store16(stg, lane, k, static_cast<uint16_t *>(s.out3) + at, s.ld, rv, cv, 1);
+                        if (mine) {
+                            store16(w, static_cast<uint16_t *>(s.out) + at, cv, bytes);
+                            store16(g, static_cast<uint16_t *>(s.out2) + at, cv, bytes);
+                            store16(k, static_cast<uint16_t *>(s.out3) + at, cv, bytes);
+                        }
                     }
                 } else {
                     tmem_ld32(tq + slot * BN + c, v);
-                    if (t.klen == 0) {   // nothing was accumulated: an empty group's sum
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = 0.f;
-                    }
                     if constexpr (EPI == EPI_ROWS) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                        store16(stg, lane, w, static_cast<uint16_t *>(s.out) + at, s.ld, rv, cv, 1);
-                    } else if constexpr (EPI == EPI_DW) {
-                        store_dw(stg, lane, v, s, at, rv, cv);
-                        store_dw(stg, lane, v + 16, s, at + 16, rv, cv - 16);
-                    } else {
+                        if (mine)
+                            store16(w, static_cast<uint16_t *>(s.out) + at, cv, bytes);
+                    } else if constexpr (EPI == EPI_NS) {
                         float alpha = s.alpha, beta = s.beta;
                         if (s.scale) {
                             const float sc = s.scale[t.g];
                             alpha = s.scale_pow == 2 ? alpha / sc / sc : alpha / sc;
                             beta /= sc;
                         }
-                        ns_values(s, t.g, alpha, beta, m + lane, t.n0 + c, rv, cv, lane, v);
+                        ns_values(s, t.g, alpha, beta, m + lane, t.n0 + c, mine, cv, v);
                         uint16_t *hi = static_cast<uint16_t *>(s.out) + at;
                         if (s.out_bf16) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                            store16(stg, lane, w, hi, s.ld, rv, cv, s.vec);
+                            if (mine)
+                                store16(w, hi, cv, bytes);
                             continue;
                         }
                         uint32_t lw[16];
@@ -747,11 +889,12 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
                         }
                         // columns past N up to the pitch's multiple of 8 are written too
                         const int cw = (cv + 7) & ~7;
-                        store16(stg, lane, w, hi, s.ld, rv, cw, 1);
+                        if (!mine)
+                            continue;
+                        store16(w, hi, cw, bytes);
                         if (s.out2)
-                            store16(stg, lane, lw, static_cast<uint16_t *>(s.out2) + at, s.ld, rv,
-                                    cw, 1);
-                        if (s.sym && t.n0 + BN <= t.m0 && lane < rv) {
+                            store16(lw, static_cast<uint16_t *>(s.out2) + at, cw, bytes);
+                        if (s.sym && t.n0 + BN <= t.m0) {
                             // the mirrored place: a column is contiguous over the lanes
                             const int64_t mt = (int64_t)t.g * s.out_group +
                                                (int64_t)(t.n0 + c) * s.ld + m + lane;
@@ -810,7 +953,7 @@ cudaError_t launch_one(const Params &p, cudaStream_t s)
         return err;
     int units = device_sms();
     if (CTAS == 2) {
-        err = cached_active_clusters((const void *)kern, THREADS, S::SMEM, 2, &units);
+        err = cached_active_clusters((const void *)kern, S::THREADS, S::SMEM, 2, &units);
         if (err != cudaSuccess)
             return err;
         if (units < 1)
@@ -825,7 +968,7 @@ cudaError_t launch_one(const Params &p, cudaStream_t s)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(CTAS * units);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(S::THREADS);
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -865,7 +1008,16 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t
 {
     int ents = 0;
     for (int i = 0; i < p.nsets; ++i) {
-        p.set[i].ent0 = ents;
+        Set &v = p.set[i];
+        v.ent0 = ents;
+        // what every row of every output (and addend) is aligned to
+        const int64_t esz = epi == EPI_DW && v.out_f32 ? 4 : 2;
+        const uint64_t all = (uint64_t)(v.ld * esz) | (uint64_t)(v.out_group * esz) |
+                             reinterpret_cast<uint64_t>(v.out) |
+                             reinterpret_cast<uint64_t>(v.out2) |
+                             reinterpret_cast<uint64_t>(v.out3) |
+                             reinterpret_cast<uint64_t>(v.add);
+        v.bytes = all % 32 == 0 ? 32 : (all % 16 == 0 ? 16 : 2);
         ents += p.set[i].groups;
     }
     if (ents > kEntries)

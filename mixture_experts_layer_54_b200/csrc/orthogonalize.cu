@@ -342,7 +342,6 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
             t.out_bf16 = 1;
             t.ld = n;
             t.out_group = mn;
-            t.vec = n % 8 == 0 && (reinterpret_cast<uintptr_t>(U) & 15u) == 0;
         } else {
             // the next step reads a low half unless it is the last
             t.out = w.X[cur ^ 1][0];
