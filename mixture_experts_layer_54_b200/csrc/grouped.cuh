@@ -85,9 +85,10 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t
 bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
            int64_t groups, int64_t group_stride, int box_rows);
 bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-            int64_t groups, int64_t group_stride);
-// Rows of the B box of a K-major operand in launches of this shape.
+            int64_t groups, int64_t group_stride, int box_rows);
+// Box rows of a K-major B, and of an MN-major operand, in launches of this shape.
 int b_box_rows(Epi epi, bool pair);
+int mn_box_rows(Epi epi, bool pair);
 
 }  // namespace grp
 }  // namespace moe

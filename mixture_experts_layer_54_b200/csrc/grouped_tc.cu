@@ -8,8 +8,8 @@
 // cluster: 256 output rows (128 a CTA) x BN columns, each CTA loading its rows
 // of A and half the rows of B.  Operands whose contraction index is the row
 // index of the stored matrix (W in dx, both in dW) are read as they lie: boxes
-// of 64 contiguous elements x 64 contraction rows, and the MMA takes them as
-// MN-major, so nothing is transposed in memory.
+// of 64 contiguous elements x a stage's contraction rows, and the MMA takes
+// them as MN-major, so nothing is transposed in memory.
 //
 // Ragged contractions (dW): a group's rows end anywhere, and what follows
 // belongs to the next group or to nobody (it may hold NaN, so it cannot be
@@ -63,6 +63,7 @@ struct Shape {
     static constexpr int KSUB = 6 * SUB <= RING_BYTES ? 2 : 1;
     static constexpr int STAGES = RING_BYTES / (KSUB * SUB) > 6 ? 6 : RING_BYTES / (KSUB * SUB);
     static constexpr int BK = 64 * KSUB;
+    static constexpr int MN_BLOCK = BK * 128;            // 64 columns of an MN-major stage
     static constexpr int OFF_B = STAGES * KSUB * A_BYTES;
     static constexpr int OFF_BAR = OFF_B + STAGES * KSUB * B_BYTES;
     static constexpr int OFF_TAB = OFF_BAR + 256;
@@ -145,10 +146,10 @@ __device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const
 
 // MN-major operand, 128-byte swizzle: 64 contiguous elements per 128-byte row,
 // one row per contraction index; 8-row groups 1024 bytes apart (stride offset),
-// blocks of 64 elements 8192 bytes apart (leading offset).
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
+// blocks of 64 elements `block` bytes apart (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block)
 {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) |
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) |
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
@@ -477,8 +478,12 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
         int issued = 0;
         uint32_t last_phase = 0;   // bit s: phase of stage s's last use
         bool ok = true;
+        Tile next;
+        if (unit < total)
+            next = decode<BM, BN>(p, tstart, span, unit);
         for (int tile = unit; ok && tile < total; tile += units) {
-            const Tile t = decode<BM, BN>(p, tstart, span, tile);
+            const Tile t = next;
+            bool ahead = false;   // the next tile is looked up behind this one's first stage
             const Set &s = p.set[t.set];
             const int m_row = t.m0 + (int)rank * 128 + (s.mode == RAGGED_M ? t.row0 : 0);
             const int segs = ACT ? 2 : s.segs;
@@ -503,9 +508,15 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     }
                     const int rem = t.klen - kb * S::BK;
                     const int nks = rem >= S::BK ? KSUB : (rem + 63) / 64;
-                    const uint32_t bytes = (uint32_t)nks * (A_BYTES + b_rows * 128);
+                    // K-major: nks boxes of 64 of K; MN-major: one box of BK per 64 columns
+                    const uint32_t bytes =
+                        (uint32_t)((A_MN ? KSUB : nks) * A_BYTES +
+                                   (b_mn ? KSUB : nks) * b_rows * 128);
                     const uint32_t fb = CTAS == 2 ? map_to_rank(full_bar(stage), 0)
                                                   : full_bar(stage);
+                    const uint32_t sa = sA + stage * KSUB * A_BYTES;
+                    const uint32_t sb = sB + stage * KSUB * S::B_BYTES;
+                    const int kc = t.k0 + kb * S::BK;
                     // rows behind the group's last must be cleared before use
                     const bool tail = A_MN && s.mode == RAGGED_K && rem < S::BK && (rem & 15);
                     if (lane == 0) {
@@ -513,31 +524,29 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                             mbar_expect_tx(tail_bar, bytes);
                         else
                             arrive_bytes<CTAS>(fb, bytes);
-                        for (int ks = 0; ks < nks; ++ks) {
-                            const int kc = t.k0 + kb * S::BK + ks * 64;
-                            const uint32_t da = sA + (stage * KSUB + ks) * A_BYTES;
-                            const uint32_t db = sB + (stage * KSUB + ks) * S::B_BYTES;
-                            auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1,
-                                            int c2) {
-                                if (tail)
-                                    tma_load_3d(dst, m, tail_bar, c0, c1, c2);
-                                else
-                                    load_box<CTAS>(dst, m, fb, c0, c1, c2);
-                            };
-                            if (A_MN) {
-                                load(da, am, m_row, kc, ga);
-                                load(da + 8192, am, m_row + 64, kc, ga);
-                            } else {
-                                load(da, am, kc, m_row, ga);
-                            }
-                            if (b_mn) {
-                                for (int b = 0; b < b_rows / 64; ++b)
-                                    load(db + b * 8192, bm, b_row + b * 64, kc, gb);
-                            } else if (uv && CTAS == 1) {
-                                load(db, bm, kc, b_row, gb);
-                                load(db + BN * 128, &s.b3, kc, b_row, gb);
-                            } else {
-                                load(db, bm, kc, b_row, gb);
+                        auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1,
+                                        int c2) {
+                            if (A_MN && tail)
+                                tma_load_3d(dst, m, tail_bar, c0, c1, c2);
+                            else
+                                load_box<CTAS>(dst, m, fb, c0, c1, c2);
+                        };
+                        if (A_MN) {
+                            load(sa, am, m_row, kc, ga);
+                            load(sa + S::MN_BLOCK, am, m_row + 64, kc, ga);
+                        } else {
+                            for (int ks = 0; ks < nks; ++ks)
+                                load(sa + ks * A_BYTES, am, kc + ks * 64, m_row, ga);
+                        }
+                        if (b_mn) {
+                            for (int b = 0; b < b_rows / 64; ++b)
+                                load(sb + b * S::MN_BLOCK, bm, b_row + b * 64, kc, gb);
+                        } else {
+                            for (int ks = 0; ks < nks; ++ks) {
+                                load(sb + ks * S::B_BYTES, bm, kc + ks * 64, b_row, gb);
+                                if (uv && CTAS == 1)
+                                    load(sb + ks * S::B_BYTES + BN * 128, &s.b3, kc + ks * 64,
+                                         b_row, gb);
                             }
                         }
                     }
@@ -545,15 +554,13 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                         okw = lane == 0 ? (wait_bar(tail_bar, tail_phase, ctl, false) ? 1 : 0) : 1;
                         okw = __shfl_sync(0xffffffffu, okw, 0);
                         tail_phase ^= 1u;
-                        const int ks = (rem - 1) / 64, r0 = rem - ks * 64;
-                        const int n = (16 - (r0 & 15)) * 8;   // 16-byte pieces per 64-wide box
-                        const uint32_t da = sA + (stage * KSUB + ks) * A_BYTES + r0 * 128;
-                        const uint32_t db = sB + (stage * KSUB + ks) * S::B_BYTES + r0 * 128;
+                        const int n = (16 - (rem & 15)) * 8;   // 16-byte pieces per 64 columns
                         const int boxes = 2 + b_rows / 64;
                         for (int i = lane; i < n * boxes; i += 32) {
                             const int box = i / n;
-                            const uint32_t dst =
-                                (box < 2 ? da + box * 8192 : db + (box - 2) * 8192) + (i % n) * 16;
+                            const uint32_t dst = (box < 2 ? sa + box * S::MN_BLOCK
+                                                          : sb + (box - 2) * S::MN_BLOCK) +
+                                                 rem * 128 + (i % n) * 16;
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst),
                                          "r"(0)
                                          : "memory");
@@ -567,6 +574,9 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                             break;
                         }
                     }
+                    if (!ahead && tile + units < total)
+                        next = decode<BM, BN>(p, tstart, span, tile + units);
+                    ahead = true;
                     issued |= 1 << stage;
                     last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) {
@@ -575,6 +585,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     }
                 }
             }
+            if (!ahead && tile + units < total)   // an empty contraction
+                next = decode<BM, BN>(p, tstart, span, tile + units);
         }
         // the leader's full barriers count both CTAs' bytes: drain there
         if (leader && lane == 0)
@@ -590,8 +602,12 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
             uint32_t phase = 0;
             int it = 0;
             bool ok = true, any = false;
+            Tile next;
+            if (unit < total)
+                next = decode<BM, BN>(p, tstart, span, unit);
             for (int tile = unit; ok && tile < total; tile += units, ++it) {
-                const Tile t = decode<BM, BN>(p, tstart, span, tile);
+                const Tile t = next;
+                bool ahead = false;
                 const Set &s = p.set[t.set];
                 int slot = it & 1;
                 if (!wait_bar(tempty_bar(slot), ((it >> 1) & 1) ^ 1u, ctl)) {
@@ -654,15 +670,21 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                             if (st >= steps)
                                 break;
                             const int ks = st >> 2, kk = st & 3;
-                            const uint32_t a = sA + (stage * KSUB + ks) * A_BYTES;
-                            const uint32_t b = sB + (stage * KSUB + ks) * S::B_BYTES;
-                            mma<CTAS>(d, A_MN ? sdesc_mn(a + kk * 2048) : sdesc_sw128(a + kk * 32),
-                                      b_mn ? sdesc_mn(b + kk * 2048) : sdesc_sw128(b + kk * 32),
+                            const uint32_t a = sA + stage * KSUB * A_BYTES;
+                            const uint32_t b = sB + stage * KSUB * S::B_BYTES;
+                            mma<CTAS>(d,
+                                      A_MN ? sdesc_mn(a + st * 2048, S::MN_BLOCK)
+                                           : sdesc_sw128(a + ks * A_BYTES + kk * 32),
+                                      b_mn ? sdesc_mn(b + st * 2048, S::MN_BLOCK)
+                                           : sdesc_sw128(b + ks * S::B_BYTES + kk * 32),
                                       idesc, first ? 0u : 1u);
                             first = false;
                         }
                         commit_all<CTAS>(empty_bar(stage));
                         any = true;
+                        if (!ahead && tile + units < total)
+                            next = decode<BM, BN>(p, tstart, span, tile + units);
+                        ahead = true;
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -671,6 +693,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                 }
                 if (!ok)
                     break;
+                if (!ahead && tile + units < total)   // an empty contraction
+                    next = decode<BM, BN>(p, tstart, span, tile + units);
                 commit_all<CTAS>(tfull_bar(slot));
                 any = true;
             }
@@ -946,6 +970,8 @@ cudaError_t launch_one(const Params &p, cudaStream_t s)
 {
     using S = Shape<CTAS, BN, EPI>;
     static_assert(S::SMEM <= 232448, "shared memory");
+    // mn_box_rows: the rows of a stage
+    static_assert(S::BK == (EPI == EPI_SWIGLU && CTAS == 1 ? 64 : 128), "stage");
     static_assert(S::DH_COL + 2 * BN <= 512 || !S::ACT, "TMEM");
     auto kern = grouped_kernel<CTAS, BN, A_MN, B_MN, EPI>;
     cudaError_t err = raise_smem_limit((const void *)kern, S::SMEM);
@@ -989,9 +1015,9 @@ bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t
 }
 
 bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-            int64_t groups, int64_t group_stride)
+            int64_t groups, int64_t group_stride, int box_rows)
 {
-    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 64, 64,
+    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 64, box_rows,
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -1003,6 +1029,8 @@ int b_box_rows(Epi epi, bool pair)
         return pair ? kBnAct / 2 : kBnAct;
     return pair ? kBnPair / 2 : kBnOne;
 }
+
+int mn_box_rows(Epi epi, bool pair) { return epi == EPI_SWIGLU && !pair ? 64 : 128; }
 
 cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t s)
 {

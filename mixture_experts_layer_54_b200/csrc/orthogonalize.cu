@@ -237,7 +237,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     if (err != cudaSuccess)
         return err;
     const bool pair = p >= 256;
-    const int box = b_box_rows(EPI_NS, pair);
+    const int box = b_box_rows(EPI_NS, pair), mbox = mn_box_rows(EPI_NS, pair);
     int cur = 0;
     for (int i = 0; i < steps; ++i, cur ^= 1) {
         const bool split = i + 1 < steps, last = i + 1 == steps;
@@ -268,7 +268,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
                 ok &= map_k(&t.a[j], X[j], m, n, ldx, E, m * ldx, 128);
                 ok &= map_k(&t.b[j], X[j], m, n, ldx, E, m * ldx, box);
             } else {
-                ok &= map_mn(&t.a[j], X[j], m, n, ldx, E, m * ldx);
+                ok &= map_mn(&t.a[j], X[j], m, n, ldx, E, m * ldx, mbox);
                 t.b[j] = t.a[j];
             }
         }
@@ -319,7 +319,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
             if (wide) {
                 ok &= map_k(&t.a[j], w.B[j], p, p, lda, E, p * lda, 128);
                 if (j == 0 || xlo)
-                    ok &= map_mn(&t.b[j], X[j], m, n, ldx, E, m * ldx);
+                    ok &= map_mn(&t.b[j], X[j], m, n, ldx, E, m * ldx, mbox);
             } else {
                 if (j == 0 || xlo)
                     ok &= map_k(&t.a[j], X[j], m, n, ldx, E, m * ldx, 128);

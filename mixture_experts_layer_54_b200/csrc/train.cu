@@ -74,7 +74,7 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
     a.out = out;
     bool ok = map_k(&a.a[0], in, R, a.K, a.K, 1, 0, 128);
     if (back)
-        ok &= map_mn(&a.b[0], W, N, K, K, G, (int64_t)N * K);
+        ok &= map_mn(&a.b[0], W, N, K, K, G, (int64_t)N * K, mn_box_rows(EPI_ROWS, pair));
     else
         ok &= map_k(&a.b[0], W, N, K, K, G, (int64_t)N * K, b_box_rows(EPI_ROWS, pair));
     if (!ok)
@@ -84,7 +84,7 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
 
 // One weight-gradient set: out[g] (M x N) (= add +) sum_r a[r, :]^T b[r, :].
 bool dw_set(Set &t, int mode, int groups, int64_t rows, int M, int N, const void *a, bool a_grouped,
-            const void *b, bool b_grouped, const void *add, void *out, bool f32)
+            const void *b, bool b_grouped, const void *add, void *out, bool f32, int box)
 {
     t.mode = mode;
     t.groups = groups;
@@ -102,8 +102,8 @@ bool dw_set(Set &t, int mode, int groups, int64_t rows, int M, int N, const void
     // no rows: nothing is loaded, the maps only have to be valid
     const int64_t r = rows > 0 ? rows : 1;
     const void *pa = rows > 0 ? a : out, *pb = rows > 0 ? b : out;
-    return map_mn(&t.a[0], pa, r, M, M, a_grouped ? groups : 1, r * M) &&
-           map_mn(&t.b[0], pb, r, N, N, b_grouped ? groups : 1, r * N);
+    return map_mn(&t.a[0], pa, r, M, M, a_grouped ? groups : 1, r * M, box) &&
+           map_mn(&t.b[0], pb, r, N, N, b_grouped ? groups : 1, r * N, box);
 }
 
 Simt simt_rows(const Table &t, int mode, int G, int M, int N, int K, const float *in,
@@ -279,7 +279,8 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         ok &= map_k(&v.a[0], dout, rows, d, d, 1, 0, 128);
         ok &= map_k(&v.a[1], in, rows, d, d, 1, 0, 128);
         ok &= map_k(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d, ubox);
-        ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d);
+        ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d,
+                     mn_box_rows(epi, pair));
         if (swiglu)
             ok &= map_k(&v.b3, w3, cols, d, d, groups, (int64_t)cols * d, ubox);
     };
@@ -313,10 +314,12 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         v.out = out;
         const int ag = mode == DENSE ? groups : 1;
         ok &= map_k(&v.a[0], du, rows, cols, cols, ag, rows * cols, 128);
-        ok &= map_mn(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d);
+        ok &= map_mn(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d,
+                     mn_box_rows(EPI_ROWS, pair));
         if (swiglu) {
             ok &= map_k(&v.a[1], dv, rows, cols, cols, ag, rows * cols, 128);
-            ok &= map_mn(&v.b[1], w3, cols, d, d, groups, (int64_t)cols * d);
+            ok &= map_mn(&v.b[1], w3, cols, d, d, groups, (int64_t)cols * d,
+                         mn_box_rows(EPI_ROWS, pair));
         }
     };
     dx_set(p.set[0], RAGGED_M, E, R, F, f.du, f.dv, a.W1, a.W3, a.dx);
@@ -333,26 +336,28 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     // weight gradients
     p = tc_params(t, status, false);
     int n = 0;
+    const bool dw_pair = pair_dw(F, d);
+    const int box = mn_box_rows(EPI_DW, dw_pair);
     auto add = [&](void *out) { return acc ? out : nullptr; };
     ok &= dw_set(p.set[n++], RAGGED_K, E, R, F, d, f.du, false, a.x_perm, false, add(a.dW1), a.dW1,
-                 f32);
+                 f32, box);
     if (swiglu)
         ok &= dw_set(p.set[n++], RAGGED_K, E, R, F, d, f.dv, false, a.x_perm, false, add(a.dW3),
-                     a.dW3, f32);
-    ok &= dw_set(p.set[n++], RAGGED_K, E, R, d, F, a.dY, false, f.h, false, add(a.dW2), a.dW2, f32);
+                     a.dW3, f32, box);
+    ok &= dw_set(p.set[n++], RAGGED_K, E, R, d, F, a.dY, false, f.h, false, add(a.dW2), a.dW2, f32, box);
     if (S > 0) {
         ok &= dw_set(p.set[n++], DENSE, S, T, Fs, d, f.dus, true, a.x, false, add(a.dWs1), a.dWs1,
-                     f32);
+                     f32, box);
         if (swiglu)
             ok &= dw_set(p.set[n++], DENSE, S, T, Fs, d, f.dvs, true, a.x, false, add(a.dWs3),
-                         a.dWs3, f32);
+                         a.dWs3, f32, box);
         ok &= dw_set(p.set[n++], DENSE, S, T, d, Fs, a.dy, false, f.hs, true, add(a.dWs2), a.dWs2,
-                     f32);
+                     f32, box);
     }
     p.nsets = n;
     if (!ok)
         return cudaErrorInvalidValue;
-    return launch_tc(p, EPI_DW, A_MN_B_MN, pair_dw(F, d), s);
+    return launch_tc(p, EPI_DW, A_MN_B_MN, dw_pair, s);
 }
 
 // fp32: the same gradients one product at a time; h holds u until the
@@ -469,11 +474,12 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
         return cuda_status(e);
     }
     Params p = tc_params(t, ws, true);
+    const bool pair = pair_dw(N, K);
     p.nsets = 1;
     if (!dw_set(p.set[0], RAGGED_K, G, R, N, K, dy, false, x, false, add, dW,
-                dw_dtype == MOE_DTYPE_F32))
+                dw_dtype == MOE_DTYPE_F32, mn_box_rows(EPI_DW, pair)))
         return MOE_ERR_CUDA;
-    return cuda_status(launch_tc(p, EPI_DW, A_MN_B_MN, pair_dw(N, K), s));
+    return cuda_status(launch_tc(p, EPI_DW, A_MN_B_MN, pair, s));
 }
 
 moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *Y_perm,
