@@ -588,9 +588,9 @@ size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t
  *   1.5, -0.5, 0 do (fp16 intermediates).  1 <= E <= 1024, m, n <= 2^20, 1 <=
  *   steps <= 32.  A matrix of zeros gives zeros; one with an infinity or NaN
  *   gives NaN, in its own update only.
- * Intermediates are pairs of fp16 terms except in the last step: the result is
- * that of 64-bit arithmetic within about 1e-3 (relative, 2-norm), then rounded
- * to bf16.
+ * The products take fp16 operands (X itself is held as two fp16 terms): the
+ * result is that of 64-bit arithmetic within about 2e-3 (relative, 2-norm), then
+ * rounded to bf16.
  */
 moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, const void *G,
                              int32_t steps, const float *coeffs, float eps, float scale, void *U,

@@ -20,30 +20,30 @@ constexpr int kEntries = 1024;   // (set, group) pairs of a launch
 
 // One family of products of a launch: out[g] = sum over K segments of A B^T.
 struct Set {
-    // Segment i of a tile's contraction multiplies operand pair i % period:
-    // A map (seg_a >> i % period) & 1, B map (seg_b >> i % period) & 1; with
+    // Segment i of a tile's contraction multiplies operand pair i % period; with
     // seg_grouped both operands' group is i / period.
     CUtensorMap a[2], b[2];
     CUtensorMap b3;              // EPI_SWIGLU: W3 (b[0] = W1, b[1] = W2)
     int mode, groups, ent0;      // ent0: first entry of the tile table
     int M, N, K;                 // output rows (not RAGGED_M), columns, contraction (not RAGGED_K)
-    int segs, period, seg_a, seg_b, seg_grouped;
+    int segs, period, seg_grouped;
     int a_grouped, b_grouped;    // 1: the operand has one matrix per group
     int sym;                     // 1: out is symmetric; only tiles on or below the diagonal
     int ld;                      // row pitch of out (elements)
     int64_t out_group;           // elements between the groups' outputs (not RAGGED_M)
     void *out;                   // EPI_GELU / EPI_SWIGLU: h
-    void *out2, *out3;           // EPI_GELU / EPI_SWIGLU: du, dv; EPI_NS: out2 = low halves
+    void *out2, *out3;           // EPI_GELU / EPI_SWIGLU: du, dv; EPI_NS: out2
     const void *add;             // EPI_DW, nullable: added before the rounding
     int out_f32;                 // EPI_DW
-    // EPI_NS: val = alpha acc + beta base; see orthogonalize.cu
-    const void *base, *base2;    // nullable high and low halves, at the transposed place if base_t
-    int base_ld, base_t, out_bf16;
+    // EPI_NS: val = alpha acc + beta base, stored as fp16 (out2: what the
+    // rounding lost, as another fp16) or as bf16
+    const void *base, *base2;    // nullable; base2: base's own second term
+    int base_ld, out_bf16;
     int64_t base_group;
     float alpha, beta;
-    const float *scale;          // nullable: scale[g] divides as scale_pow says
-    int scale_pow;               // val = alpha / s^pow acc + beta / s base (s once for pow < 2)
-    int bytes;                   // alignment of the output rows (32, 16 or 2), found at launch
+    const float *scale;          // nullable: alpha / scale[g]^scale_pow, beta / scale[g]
+    int scale_pow;
+    int bytes, base_bytes;       // alignment of the rows (32, 16 or 2), found at launch
 };
 
 struct __align__(64) Params {

@@ -315,57 +315,55 @@ __device__ __forceinline__ float2 unpack_fp16(uint32_t u)
     return __half22float2(*reinterpret_cast<__half2 *>(&u));
 }
 
-// val = alpha acc + beta base for 32 columns of this lane's row.  base_t reads
-// the (symmetric) base at the transposed place, where a column is contiguous
-// over the warp's rows.
-__device__ __forceinline__ void ns_values(const Set &s, int g, float alpha, float beta, int row,
-                                          int col, bool mine, int cv, float *v)
+// val = alpha acc + beta base for 32 columns of this lane's row.
+__device__ __forceinline__ void ns_values(const Set &s, int64_t at, float alpha, float beta, int cv,
+                                          float *v)
 {
+    uint32_t b[16];
+    const uint8_t *hi = reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base) + at);
+    load_row<2>(hi, 2 * cv, s.base_bytes, b);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] *= alpha;
-    if (!s.base || !mine)
-        return;
-    const int64_t g0 = (int64_t)g * s.base_group;
-    const __half *hi = static_cast<const __half *>(s.base) + g0;
-    const __half *lo = s.base2 ? static_cast<const __half *>(s.base2) + g0 : nullptr;
-    if (s.base_t) {
+    for (int i = 0; i < 16; ++i) {
+        const float2 f = unpack_fp16(b[i]);
+        v[2 * i] += beta * f.x;
+        v[2 * i + 1] += beta * f.y;
+    }
+    if (s.base2) {
+        const uint8_t *lo =
+            reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base2) + at);
+        load_row<2>(lo, 2 * cv, s.base_bytes, b);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i < cv) {
-                const int64_t o = (int64_t)(col + i) * s.base_ld + row;
-                float b = __half2float(hi[o]);
-                if (lo)
-                    b += __half2float(lo[o]);
-                v[i] += beta * b;
-            }
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = unpack_fp16(b[i]);
+            v[2 * i] += beta * f.x;
+            v[2 * i + 1] += beta * f.y;
         }
-    } else {
-        const int64_t o = (int64_t)row * s.base_ld + col;
+    }
+}
+
+// The mirrored place of 32 columns (w: pairs of columns of this lane's row):
+// out points at column 0's place for row 0 of the warp.  Two exchanges give a
+// lane one column's values for four rows, so a warp stores 64-byte pieces, 8
+// bytes a lane.  rv rows and cv columns are valid (the pitch covers rv rounded
+// up to 4).
+__device__ __forceinline__ void store_mirror(const uint32_t *w, uint16_t *out, int64_t ld, int lane,
+                                             int rv, int cv)
+{
+    uint32_t y[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (c * 8 >= cv)
-                continue;
-            // the pitch is a multiple of 8 and holds at least cv rounded up to it
-            const uint4 h = *reinterpret_cast<const uint4 *>(hi + o + 8 * c);
-            const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
+        y[j] = lane & 1 ? __byte_perm(o, w[j], 0x7632) : __byte_perm(w[j], o, 0x5410);
+    }
+    const bool up = lane & 2;
+    const int r = lane & ~3;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack_fp16(w[j]);
-                v[8 * c + 2 * j] += beta * f.x;
-                v[8 * c + 2 * j + 1] += beta * f.y;
-            }
-            if (lo) {
-                const uint4 l = *reinterpret_cast<const uint4 *>(lo + o + 8 * c);
-                const uint32_t x[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack_fp16(x[j]);
-                    v[8 * c + 2 * j] += beta * f.x;
-                    v[8 * c + 2 * j + 1] += beta * f.y;
-                }
-            }
-        }
+    for (int j = 0; j < 16; j += 2) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 1], 2);
+        const int col = 2 * j + (up ? 2 : 0) + (lane & 1);
+        if (r < rv && col < cv)
+            *reinterpret_cast<uint2 *>(out + col * ld + r) =
+                up ? make_uint2(o, y[j + 1]) : make_uint2(y[j], o);
     }
 }
 
@@ -489,8 +487,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
             const int segs = ACT ? 2 : s.segs;
             for (int sg = 0; ok && sg < segs; ++sg) {
                 const int ph = ACT ? sg : sg % s.period;
-                const int ai = ACT ? sg : (s.seg_a >> ph) & 1;
-                const int bi = ACT ? 1 - sg : (s.seg_b >> ph) & 1;
+                const int bi = ACT ? 1 - sg : ph;
                 const int grp = !ACT && s.seg_grouped ? sg / s.period : t.g;
                 const int ga = s.a_grouped ? grp : 0, gb = s.b_grouped ? grp : 0;
                 const bool uv = EPI == EPI_SWIGLU && sg == 1;
@@ -498,7 +495,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                 // B rows of this CTA, and their first
                 const int b_rows = ACT ? (uv ? S::B_ROWS : BN / CTAS) : S::B_ROWS;
                 const int b_row = t.n0 + (uv && CTAS == 2 ? 0 : (int)rank * (BN / CTAS));
-                const CUtensorMap *am = &s.a[ai];
+                const CUtensorMap *am = &s.a[ph];
                 const CUtensorMap *bm = uv && rank == 1 ? &s.b3 : &s.b[bi];
                 for (int kb = 0; kb * S::BK < t.klen; ++kb) {
                     int okw = lane == 0 ? (wait_bar(empty_bar(stage), phase ^ 1u, ctl) ? 1 : 0) : 1;
@@ -894,7 +891,13 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                             alpha = s.scale_pow == 2 ? alpha / sc / sc : alpha / sc;
                             beta /= sc;
                         }
-                        ns_values(s, t.g, alpha, beta, m + lane, t.n0 + c, mine, cv, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] *= alpha;
+                        if (s.base && mine)
+                            ns_values(s,
+                                      (int64_t)t.g * s.base_group + row * s.base_ld + t.n0 + c,
+                                      alpha, beta, cv, v);
                         uint16_t *hi = static_cast<uint16_t *>(s.out) + at;
                         if (s.out_bf16) {
 #pragma unroll
@@ -904,35 +907,29 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                                 store16(w, hi, cv, bytes);
                             continue;
                         }
-                        uint32_t lw[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 16; ++i)
                             w[i] = pack_fp16(v[2 * i], v[2 * i + 1]);
-                            const float2 f = unpack_fp16(w[i]);
-                            lw[i] = pack_fp16(v[2 * i] - f.x, v[2 * i + 1] - f.y);
-                        }
                         // columns past N up to the pitch's multiple of 8 are written too
                         const int cw = (cv + 7) & ~7;
-                        if (!mine)
-                            continue;
-                        store16(w, hi, cw, bytes);
-                        if (s.out2)
-                            store16(lw, static_cast<uint16_t *>(s.out2) + at, cw, bytes);
-                        if (s.sym && t.n0 + BN <= t.m0) {
-                            // the mirrored place: a column is contiguous over the lanes
-                            const int64_t mt = (int64_t)t.g * s.out_group +
-                                               (int64_t)(t.n0 + c) * s.ld + m + lane;
-                            uint16_t *mh = static_cast<uint16_t *>(s.out) + mt;
-                            uint16_t *ml = static_cast<uint16_t *>(s.out2) + mt;
+                        if (mine)
+                            store16(w, hi, cw, bytes);
+                        if (s.out2) {
+                            uint32_t lw[16];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < cv) {
-                                    mh[(int64_t)i * s.ld] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-                                    if (s.out2)
-                                        ml[(int64_t)i * s.ld] =
-                                            (uint16_t)(lw[i / 2] >> (16 * (i & 1)));
-                                }
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 f = unpack_fp16(w[i]);
+                                lw[i] = pack_fp16(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+                            }
+                            if (mine)
+                                store16(lw, static_cast<uint16_t *>(s.out2) + at, cw, bytes);
                         }
+                        if (s.sym && t.n0 + BN <= t.m0)
+                            store_mirror(w,
+                                         static_cast<uint16_t *>(s.out) +
+                                             (int64_t)t.g * s.out_group +
+                                             (int64_t)(t.n0 + c) * s.ld + m,
+                                         s.ld, lane, rv, cv);
                     }
                 }
             }
@@ -1046,6 +1043,10 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t
                              reinterpret_cast<uint64_t>(v.out3) |
                              reinterpret_cast<uint64_t>(v.add);
         v.bytes = all % 32 == 0 ? 32 : (all % 16 == 0 ? 16 : 2);
+        const uint64_t base = (uint64_t)(v.base_ld * 2) | (uint64_t)(v.base_group * 2) |
+                              reinterpret_cast<uint64_t>(v.base) |
+                              reinterpret_cast<uint64_t>(v.base2);
+        v.base_bytes = base % 32 == 0 ? 32 : 16;
         ents += p.set[i].groups;
     }
     if (ents > kEntries)

@@ -4,18 +4,20 @@
 // which drives the singular values towards 1 and keeps the singular vectors.
 //
 // Bound by the tensor cores.  The products run on the fp16 pipe (the rate of
-// bf16, 3 more bits), on 2-byte copies of X, A and B = b A + c A A with fixed
+// bf16, 3 more bits) on fp16 copies of X, A and B = b A + c A A with fixed
 // powers of two as scales, so nothing is near the ends of fp16's range while
-// the singular values stay below about 2.8.  One rounding to fp16 (2^-11)
-// would be enough for a step on its own, but a step multiplies small singular
-// values by a = 3.4: noise that enters in the first of five steps comes out
-// 140 times as large against a low-rank gradient (1e-2 of the result, measured
-// in 64 bits).  So every step but the last holds X, A and B as two fp16 terms
-// (hi + lo, 22 bits) and computes hi hi + hi lo + lo hi in one fp32
-// accumulator; the last step's operands are single fp16, and the result is
-// within 1e-3 of the 64-bit one before its rounding to bf16.  A bf16 G times a
-// power of two is exact in one fp16 term.  A and B are symmetric: only tiles
-// on or below the diagonal are computed and mirrored.
+// the singular values stay below about 2.8.  A step multiplies small singular
+// values by a = 3.4, so what a rounding of X (2^-11) leaves among them in the
+// first of five steps comes out 140 times as large: 2e-2 of the result for an
+// update of rank 32, measured.  That noise only passes through a X, since B
+// multiplies those directions by almost nothing; so X is held as two fp16
+// terms (hi + lo, 22 bits), a X takes both and the products only hi.  The
+// result is then within 2e-3 of the 64-bit one (2-norm; 1.6e-3 for noise, 1e-3
+// and less for decaying spectra), at the cost of one product each, where two
+// terms in every product cost 2.6 times as much for 8e-4.  The last step reads
+// hi alone: near singular value 1 the same X in both places is the more exact.
+// A bf16 G times a power of two is exact in one term.  A and B are symmetric:
+// only tiles on or below the diagonal are computed and mirrored.
 #include "grouped.cuh"
 
 #include <cuda_fp16.h>
@@ -29,7 +31,7 @@ namespace {
 
 // stored value = true value times these
 constexpr float kSX = 8192.f, kSA = 8192.f, kSB = 2048.f;
-constexpr int kMaxParts = 64;
+constexpr int kMaxParts = 256;
 
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 
@@ -68,7 +70,8 @@ __device__ __forceinline__ void load8(const T *p, int n, bool vec, float *f)
 }
 
 // Sums of squares of `parts` slices of each matrix (fp32 in a thread, then
-// double over the block; fixed order).
+// double over the block; fixed order).  Four 8-element pieces of a thread are
+// in flight at a time.
 template <typename T>
 __global__ void __launch_bounds__(256)
     square_sums_kernel(const T *G, int64_t mn, int parts, bool vec, double *out)
@@ -77,16 +80,24 @@ __global__ void __launch_bounds__(256)
     pdl_trigger();
     const int e = blockIdx.y;
     const T *g = G + e * mn;
-    float acc = 0.f;
-    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < mn; i += parts * 2048ll) {
-        float f[8];
-        load8(g + i, mn - i < 8 ? (int)(mn - i) : 8, vec, f);
+    const int64_t step = parts * 2048ll;
+    float acc[4] = {};
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < mn; i += 4 * step) {
+        float f[4][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc = fmaf(f[j], f[j], acc);
+        for (int u = 0; u < 4; ++u) {
+            const int64_t o = i + u * step;
+            const int n = mn - o < 8 ? (int)(mn - o) : 8;
+            load8(g + (n > 0 ? o : 0), n, vec, f[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc[u] = fmaf(f[u][j], f[u][j], acc[u]);
     }
     __shared__ double part[8];
-    double v = acc;
+    double v = (double)acc[0] + acc[1] + acc[2] + acc[3];
 #pragma unroll
     for (int s = 16; s; s >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, s);
@@ -102,6 +113,7 @@ __global__ void __launch_bounds__(256)
 
 // X = G 2^k as one or two fp16 terms, 2^k the power of two that brings |G| + eps
 // into (kSX / 2, kSX]; scale[e] = 2^k (|G| + eps) is then what X stands over.
+// Rows of a multiple of 8 elements are one run of them; others go row by row.
 template <typename T>
 __global__ void __launch_bounds__(256)
     scale_kernel(const T *G, int m, int n, int64_t ld, int parts, bool vec, const double *sums,
@@ -111,48 +123,70 @@ __global__ void __launch_bounds__(256)
     pdl_trigger();
     const int e = blockIdx.y;
     __shared__ float s_mul;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < 32) {
         double v = 0;
-        for (int i = 0; i < parts; ++i)
+        for (int i = threadIdx.x; i < parts; i += 32)
             v += sums[e * kMaxParts + i];
-        const double norm = sqrt(v) + (double)eps;
-        int k = 0;
-        double mul = 1.0, sc = norm;   // zero with eps = 0: 0 / 0 as the formula has it
-        if (isfinite(norm) && norm > 0) {
-            k = 13 - (int)ceil(log2(norm));
-            k = min(max(k, -126), 126);
-            mul = exp2((double)k);
-            sc = mul * norm;
-        } else if (!isfinite(norm)) {
-            sc = nan("");   // an infinity or NaN in G: the whole update is NaN
+#pragma unroll
+        for (int s = 16; s; s >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, s);
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(v) + (double)eps;
+            double mul = 1.0, sc = norm;   // zero with eps = 0: 0 / 0 as the formula has it
+            if (isfinite(norm) && norm > 0) {
+                const int k = min(max(13 - (int)ceil(log2(norm)), -126), 126);
+                mul = exp2((double)k);
+                sc = mul * norm;
+            } else if (!isfinite(norm)) {
+                sc = nan("");   // an infinity or NaN in G: the whole update is NaN
+            }
+            s_mul = (float)mul;
+            if (blockIdx.x == 0)
+                scale[e] = (float)sc;
         }
-        s_mul = (float)mul;
-        if (blockIdx.x == 0)
-            scale[e] = (float)sc;
     }
     __syncthreads();
     const float mul = s_mul;
     const int cpr = (int)(ld / 8);
     const int64_t chunks = (int64_t)m * cpr;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < chunks; i += gridDim.x * 256ll) {
-        const int64_t r = i / cpr;
-        const int c = (int)(i % cpr) * 8;
-        float f[8];
-        load8(G + ((int64_t)e * m + r) * n + c, n - c < 8 ? n - c : 8, vec, f);
-        uint32_t h[4], l[4];
+    const bool flat = n == ld;
+    const T *g = G + (int64_t)e * m * n;
+    __half *oh = hi + (int64_t)e * m * ld, *ol = lo ? lo + (int64_t)e * m * ld : nullptr;
+    const int64_t step = gridDim.x * 256ll;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < chunks; i += 2 * step) {
+        float f[2][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x0 = f[2 * j] * mul, x1 = f[2 * j + 1] * mul;
-            const __half2 a = __floats2half2_rn(x0, x1);
-            const float2 b = __half22float2(a);
-            const __half2 d = __floats2half2_rn(x0 - b.x, x1 - b.y);
-            h[j] = *reinterpret_cast<const uint32_t *>(&a);
-            l[j] = *reinterpret_cast<const uint32_t *>(&d);
+        for (int u = 0; u < 2; ++u) {
+            const int64_t k = i + u * step;
+            if (k < chunks) {
+                if (flat) {
+                    load8(g + 8 * k, 8, vec, f[u]);
+                } else {
+                    const int64_t r = k / cpr;
+                    const int c = (int)(k - r * cpr) * 8;
+                    load8(g + r * n + c, n - c < 8 ? n - c : 8, vec, f[u]);
+                }
+            }
         }
-        const int64_t o = ((int64_t)e * m + r) * ld + c;
-        *reinterpret_cast<uint4 *>(hi + o) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (lo)
-            *reinterpret_cast<uint4 *>(lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t k = i + u * step;
+            if (k >= chunks)
+                break;
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x0 = f[u][2 * j] * mul, x1 = f[u][2 * j + 1] * mul;
+                const __half2 a = __floats2half2_rn(x0, x1);
+                const float2 b = __half22float2(a);
+                const __half2 d = __floats2half2_rn(x0 - b.x, x1 - b.y);
+                h[j] = *reinterpret_cast<const uint32_t *>(&a);
+                l[j] = *reinterpret_cast<const uint32_t *>(&d);
+            }
+            *reinterpret_cast<uint4 *>(oh + 8 * k) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (ol)
+                *reinterpret_cast<uint4 *>(ol + 8 * k) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
     }
 }
 
@@ -160,7 +194,7 @@ struct Bufs {
     int32_t *status;
     double *sums;
     float *scale;
-    __half *X[2][2], *A[2], *B[2];   // [ping-pong][hi, lo]
+    __half *X[2][2], *A, *B;   // X: [ping-pong][hi, lo]
     size_t bytes;
 };
 
@@ -182,10 +216,8 @@ Bufs carve(int64_t E, int64_t m, int64_t n, int steps, void *ws)
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 2; ++j)
             b.X[i][j] = static_cast<__half *>(take(steps > 1 || i + j == 0 ? x : 0));
-    for (int j = 0; j < 2; ++j) {
-        b.A[j] = static_cast<__half *>(take(steps > 1 || j == 0 ? a : 0));
-        b.B[j] = static_cast<__half *>(take(steps > 1 || j == 0 ? a : 0));
-    }
+    b.A = static_cast<__half *>(take(a));
+    b.B = static_cast<__half *>(take(a));
     b.bytes = off;
     return b;
 }
@@ -209,7 +241,9 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     const int esz = bf16 ? 2 : 4;
     const bool al = (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
     const int64_t want = ceil_div(mn, 256 * 8 * 4);
-    const int parts = (int)(want < 1 ? 1 : (want > kMaxParts ? kMaxParts : want));
+    const int64_t cap = ceil_div(148 * 6, E);   // a few blocks an SM over all matrices
+    const int64_t most_parts = cap < kMaxParts ? cap : kMaxParts;
+    const int parts = (int)(want < 1 ? 1 : (want > most_parts ? most_parts : want));
     const bool vsum = al && mn * esz % 16 == 0, vrow = al && (int64_t)n * esz % 16 == 0;
     int64_t cblocks = ceil_div((int64_t)m * (ldx / 8), 256);
     const int64_t most = ceil_div(148 * 16, E);
@@ -240,10 +274,8 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     const int box = b_box_rows(EPI_NS, pair), mbox = mn_box_rows(EPI_NS, pair);
     int cur = 0;
     for (int i = 0; i < steps; ++i, cur ^= 1) {
-        const bool split = i + 1 < steps, last = i + 1 == steps;
-        const bool xlo = split && (i > 0 || lo0);
-        __half *const *X = w.X[cur];
-        const float xs = kSX;
+        const bool last = i + 1 == steps;
+        __half *X = w.X[cur][0], *Xlo = !last && (i > 0 || lo0) ? w.X[cur][1] : nullptr;
         bool ok = true;
         Params P;
         memset(&P, 0, sizeof P);
@@ -255,28 +287,23 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.mode = DENSE;
         t.groups = E;
         t.a_grouped = t.b_grouped = 1;
+        t.segs = t.period = 1;
 
-        // A = X X^T (X^T X): hi hi + hi lo + lo hi
+        // A = X X^T (X^T X)
         t.M = t.N = p;
         t.K = q;
         t.sym = 1;
-        t.segs = t.period = xlo ? 3 : 1;
-        t.seg_a = 4;
-        t.seg_b = 2;
-        for (int j = 0; j < (xlo ? 2 : 1); ++j) {
-            if (wide) {
-                ok &= map_k(&t.a[j], X[j], m, n, ldx, E, m * ldx, 128);
-                ok &= map_k(&t.b[j], X[j], m, n, ldx, E, m * ldx, box);
-            } else {
-                ok &= map_mn(&t.a[j], X[j], m, n, ldx, E, m * ldx, mbox);
-                t.b[j] = t.a[j];
-            }
+        if (wide) {
+            ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128);
+            ok &= map_k(&t.b[0], X, m, n, ldx, E, m * ldx, box);
+        } else {
+            ok &= map_mn(&t.a[0], X, m, n, ldx, E, m * ldx, mbox);
+            t.b[0] = t.a[0];
         }
-        t.out = w.A[0];
-        t.out2 = split ? w.A[1] : nullptr;
+        t.out = w.A;
         t.ld = (int)lda;
         t.out_group = p * lda;
-        t.alpha = i == 0 ? kSA : kSA / (xs * xs);
+        t.alpha = i == 0 ? kSA : kSA / (kSX * kSX);
         t.scale = i == 0 ? w.scale : nullptr;
         t.scale_pow = 2;
         if (!ok)
@@ -287,19 +314,13 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         // B = b A + c A A
         P.clear_status = 0;
         t.K = p;
-        t.segs = t.period = split ? 3 : 1;
-        for (int j = 0; j < (split ? 2 : 1); ++j) {
-            ok &= map_k(&t.a[j], w.A[j], p, p, lda, E, p * lda, 128);
-            ok &= map_k(&t.b[j], w.A[j], p, p, lda, E, p * lda, box);
-        }
-        t.out = w.B[0];
-        t.out2 = split ? w.B[1] : nullptr;
+        ok &= map_k(&t.a[0], w.A, p, p, lda, E, p * lda, 128);
+        ok &= map_k(&t.b[0], w.A, p, p, lda, E, p * lda, box);
+        t.out = w.B;
         t.alpha = c * kSB / (kSA * kSA);
         t.beta = b * kSB / kSA;
-        t.base = w.A[0];
-        t.base2 = split ? w.A[1] : nullptr;
+        t.base = w.A;
         t.base_ld = (int)lda;
-        t.base_t = 1;
         t.base_group = p * lda;
         t.scale = nullptr;
         if (!ok)
@@ -311,44 +332,27 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.sym = 0;
         t.M = m;
         t.N = n;
-        t.segs = t.period = split ? (xlo ? 3 : 2) : 1;
-        const int b_seg = 2, x_seg = 4;   // segment 1: low half of B; segment 2: of X
-        t.seg_a = wide ? b_seg : x_seg;
-        t.seg_b = wide ? x_seg : b_seg;
-        for (int j = 0; j < (split ? 2 : 1); ++j) {
-            if (wide) {
-                ok &= map_k(&t.a[j], w.B[j], p, p, lda, E, p * lda, 128);
-                if (j == 0 || xlo)
-                    ok &= map_mn(&t.b[j], X[j], m, n, ldx, E, m * ldx, mbox);
-            } else {
-                if (j == 0 || xlo)
-                    ok &= map_k(&t.a[j], X[j], m, n, ldx, E, m * ldx, 128);
-                ok &= map_k(&t.b[j], w.B[j], p, p, lda, E, p * lda, box);
-            }
+        if (wide) {
+            ok &= map_k(&t.a[0], w.B, p, p, lda, E, p * lda, 128);
+            ok &= map_mn(&t.b[0], X, m, n, ldx, E, m * ldx, mbox);
+        } else {
+            ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128);
+            ok &= map_k(&t.b[0], w.B, p, p, lda, E, p * lda, box);
         }
         const float mult = last ? scale : kSX;
-        t.alpha = i == 0 ? mult / kSB : mult / (kSB * xs);
-        t.beta = i == 0 ? a * mult : a * mult / xs;
+        t.alpha = i == 0 ? mult / kSB : mult / (kSB * kSX);
+        t.beta = i == 0 ? a * mult : a * mult / kSX;
         t.scale = i == 0 ? w.scale : nullptr;
         t.scale_pow = 1;
-        t.base = X[0];
-        t.base2 = xlo ? X[1] : nullptr;
+        t.base = X;
+        t.base2 = Xlo;
         t.base_ld = (int)ldx;
-        t.base_t = 0;
         t.base_group = m * ldx;
-        if (last) {
-            t.out = U;
-            t.out2 = nullptr;
-            t.out_bf16 = 1;
-            t.ld = n;
-            t.out_group = mn;
-        } else {
-            // the next step reads a low half unless it is the last
-            t.out = w.X[cur ^ 1][0];
-            t.out2 = i + 2 < steps ? w.X[cur ^ 1][1] : nullptr;
-            t.ld = (int)ldx;
-            t.out_group = m * ldx;
-        }
+        t.out = last ? U : w.X[cur ^ 1][0];
+        t.out2 = i + 2 < steps ? w.X[cur ^ 1][1] : nullptr;   // the last step reads hi alone
+        t.out_bf16 = last;
+        t.ld = last ? n : (int)ldx;
+        t.out_group = last ? mn : m * ldx;
         if (!ok)
             return cudaErrorInvalidValue;
         if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_MN : A_K_B_K, pair, s)) != cudaSuccess)

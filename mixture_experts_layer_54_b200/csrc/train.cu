@@ -307,7 +307,6 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         v.period = swiglu ? 2 : 1;
         v.segs = v.period * (mode == DENSE ? groups : 1);
         v.seg_grouped = mode == DENSE;
-        v.seg_a = v.seg_b = 2;
         v.a_grouped = mode == DENSE;
         v.b_grouped = 1;
         v.ld = d;
