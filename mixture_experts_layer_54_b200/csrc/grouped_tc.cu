@@ -315,30 +315,15 @@ __device__ __forceinline__ float2 unpack_fp16(uint32_t u)
     return __half22float2(*reinterpret_cast<__half2 *>(&u));
 }
 
-// val = alpha acc + beta base for 32 columns of this lane's row.
-__device__ __forceinline__ void ns_values(const Set &s, int64_t at, float alpha, float beta, int cv,
-                                          float *v)
+// Both terms of base, 32 columns of this lane's row from element `at` on.
+__device__ __forceinline__ void load_base(const Set &s, int64_t at, int cv, uint32_t *hi,
+                                          uint32_t *lo)
 {
-    uint32_t b[16];
-    const uint8_t *hi = reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base) + at);
-    load_row<2>(hi, 2 * cv, s.base_bytes, b);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float2 f = unpack_fp16(b[i]);
-        v[2 * i] += beta * f.x;
-        v[2 * i + 1] += beta * f.y;
-    }
-    if (s.base2) {
-        const uint8_t *lo =
-            reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base2) + at);
-        load_row<2>(lo, 2 * cv, s.base_bytes, b);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 f = unpack_fp16(b[i]);
-            v[2 * i] += beta * f.x;
-            v[2 * i + 1] += beta * f.y;
-        }
-    }
+    load_row<2>(reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base) + at), 2 * cv,
+                s.base_bytes, hi);
+    if (s.base2)
+        load_row<2>(reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base2) + at),
+                    2 * cv, s.base_bytes, lo);
 }
 
 // The mirrored place of 32 columns (w: pairs of columns of this lane's row):
@@ -711,13 +696,23 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
             const Tile t = decode<BM, BN>(p, tstart, span, tile);
             const Set &s = p.set[t.set];
             int slot = it & 1;
+            const int m = t.m0 + (int)rank * 128 + q * 32;   // first row, in the group
+            const int rv = t.mg - m;                          // rows of it from there on
+            const int c_end = rv > 0 ? min((half + 1) * (BN / 2), s.N - t.n0) : 0;
+            // base is read a chunk ahead: the first before the products are done
+            uint32_t bhi[EPI == EPI_NS ? 16 : 1], blo[EPI == EPI_NS ? 16 : 1];
+            const bool based = EPI == EPI_NS && s.base && lane < rv;
+            const int64_t base0 =
+                (int64_t)t.g * s.base_group + (int64_t)(m + lane) * s.base_ld + t.n0;
+            if constexpr (EPI == EPI_NS) {
+                const int c = half * (BN / 2);
+                if (based && c < c_end)
+                    load_base(s, base0 + c, s.N - t.n0 - c, bhi, blo);
+            }
             if (!wait_bar(tfull_bar(slot), (it >> 1) & 1, ctl))
                 break;
             tc_fence_after();
             const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
-            const int m = t.m0 + (int)rank * 128 + q * 32;   // first row, in the group
-            const int rv = t.mg - m;                          // rows of it from there on
-            const int c_end = rv > 0 ? min((half + 1) * (BN / 2), s.N - t.n0) : 0;
             const int64_t row = m + lane + (s.mode == RAGGED_M ? t.row0 : 0);
             const int64_t at0 = (s.mode == RAGGED_M ? 0 : (int64_t)t.g * s.out_group) +
                                 row * s.ld + t.n0;
@@ -894,10 +889,20 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] *= alpha;
-                        if (s.base && mine)
-                            ns_values(s,
-                                      (int64_t)t.g * s.base_group + row * s.base_ld + t.n0 + c,
-                                      alpha, beta, cv, v);
+                        if (based) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float2 f = unpack_fp16(bhi[i]);
+                                if (s.base2) {
+                                    const float2 l = unpack_fp16(blo[i]);
+                                    f.x += l.x, f.y += l.y;
+                                }
+                                v[2 * i] += beta * f.x;
+                                v[2 * i + 1] += beta * f.y;
+                            }
+                            if (c + 32 < c_end)
+                                load_base(s, base0 + c + 32, cv - 32, bhi, blo);
+                        }
                         uint16_t *hi = static_cast<uint16_t *>(s.out) + at;
                         if (s.out_bf16) {
 #pragma unroll
