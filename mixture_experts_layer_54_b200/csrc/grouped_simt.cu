@@ -17,6 +17,8 @@ __global__ void __launch_bounds__(256) simt_kernel(const Simt p)
     const int g = blockIdx.z, tid = threadIdx.x;
     pdl_wait();
     pdl_trigger();
+    if (p.clear && blockIdx.x + blockIdx.y + blockIdx.z == 0 && tid == 0)
+        *p.clear = 0;
     int M = p.M, K = p.K, m_base = 0, k_base = 0;
     if (p.mode == RAGGED_M)
         group_rows(p.offsets, p.rows, p.n_rows, g, &m_base, &M);

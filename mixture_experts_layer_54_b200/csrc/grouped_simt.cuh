@@ -19,6 +19,7 @@ struct Simt {
     int64_t a_m, a_k, a_group, b_n, b_k, b_group, c_m, c_group;
     const int32_t *offsets, *rows;
     int n_rows;
+    int32_t *clear;   // nullable: the status word, set to 0
 };
 
 cudaError_t launch_simt(const Simt &p, cudaStream_t s);

@@ -203,13 +203,10 @@ moe_status rows_call(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K, 
         return cuda_status(clear_word(ws, s));
     if (dtype == MOE_DTYPE_BF16)
         return cuda_status(rows_tc(t, G, R, N, K, in, W, out, back, ws, s));
-    cudaError_t e = clear_word(ws, s);
-    if (e == cudaSuccess)
-        e = launch_simt(simt_rows(t, RAGGED_M, G, 0, N, K, static_cast<const float *>(in), 0,
-                                  static_cast<const float *>(W), back, static_cast<float *>(out),
-                                  0, nullptr),
-                        s);
-    return cuda_status(e);
+    Simt p = simt_rows(t, RAGGED_M, G, 0, N, K, static_cast<const float *>(in), 0,
+                       static_cast<const float *>(W), back, static_cast<float *>(out), 0, nullptr);
+    p.clear = static_cast<int32_t *>(ws);
+    return cuda_status(launch_simt(p, s));
 }
 
 // Scratch of the FFN backward: hidden activations and their gradients, and in
@@ -362,12 +359,14 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
 // fp32: the same gradients one product at a time; h holds u until the
 // activation gradient, du holds dh, dv holds v.
 cudaError_t ffn_grad_simt(const moe_config &c, const Table &t, const FfnArgs &a,
-                          const FfnScratch &f, bool acc, cudaStream_t s)
+                          const FfnScratch &f, bool acc, void *status, cudaStream_t s)
 {
     const bool swiglu = c.act == MOE_ACT_SWIGLU;
     const int d = c.d;
     cudaError_t e = cudaSuccess;
-    auto run = [&](const Simt &p) {
+    auto run = [&](Simt p) {
+        p.clear = static_cast<int32_t *>(status);   // the first launch clears it
+        status = nullptr;
         if (e == cudaSuccess)
             e = launch_simt(p, s);
     };
@@ -464,13 +463,11 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Table t{offsets, rows, (int)R};
     if (dtype == MOE_DTYPE_F32) {
-        cudaError_t e = clear_word(ws, s);
-        if (e == cudaSuccess)
-            e = launch_simt(simt_dw(t, RAGGED_K, G, 0, N, K, static_cast<const float *>(dy), 0,
-                                    static_cast<const float *>(x), 0,
-                                    static_cast<const float *>(add), static_cast<float *>(dW)),
-                            s);
-        return cuda_status(e);
+        Simt p = simt_dw(t, RAGGED_K, G, 0, N, K, static_cast<const float *>(dy), 0,
+                         static_cast<const float *>(x), 0, static_cast<const float *>(add),
+                         static_cast<float *>(dW));
+        p.clear = static_cast<int32_t *>(ws);
+        return cuda_status(launch_simt(p, s));
     }
     Params p = tc_params(t, ws, true);
     const bool pair = pair_dw(N, K);
@@ -546,10 +543,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
     if (c.dtype == MOE_DTYPE_BF16)
         return cuda_status(ffn_grad_tc(c, t, a, f, dw_dtype == MOE_DTYPE_F32, accumulate != 0, ws,
                                        s));
-    cudaError_t e = clear_word(ws, s);
-    if (e == cudaSuccess)
-        e = ffn_grad_simt(c, t, a, f, accumulate != 0, s);
-    return cuda_status(e);
+    return cuda_status(ffn_grad_simt(c, t, a, f, accumulate != 0, ws, s));
 }
 
 size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t steps)

@@ -11,7 +11,7 @@ from dataclasses import dataclass
 import torch
 
 from ._abi import MoeConfig, check, lib
-from .ops import (DTYPE_BF16, DTYPE_F32, _p, _stream, _tdtype, moe_perm_rows, workspace)
+from .ops import DTYPE_BF16, DTYPE_F32, _p, _tdtype, moe_validate, workspace
 
 _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
@@ -22,11 +22,41 @@ def _code(t, what):
     return _CODES[t.dtype]
 
 
+def _ptrs(*tensors):
+    """Device addresses of the tensors (None for None), after ops._p's checks.
+    One look at the current device serves the call."""
+    dev, out = None, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if at < 0 or not t.is_contiguous():
+            _p(t)   # says what is wrong
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if at != dev:
+            _p(t)
+        out.append(t.data_ptr())
+    return out
+
+
+def _stream():
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _rows(cfg):
+    R = lib().moe_perm_rows(ctypes.byref(cfg))
+    if R < 0:
+        moe_validate(cfg)
+    return R
+
+
 def _is(t, shape, dtype, what):
     """The library reads raw buffers: a wrong shape or type is refused here."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}: "
                          f"{dtype} {tuple(shape)} wanted")
 
@@ -55,8 +85,8 @@ def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
         y = torch.empty(shape, dtype=x.dtype, device=x.device)
     _is(y, shape, x.dtype, "y")
     ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, x.device)
-    check(lib().moe_grouped_matmul(*sizes, _p(x), _p(W), _p(offsets), _p(rows), _p(y), _p(ws),
-                                   ws.numel(), _stream()), "moe_grouped_matmul")
+    check(lib().moe_grouped_matmul(*sizes, *_ptrs(x, W, offsets, rows, y, ws), ws.numel(),
+                                   _stream()), "moe_grouped_matmul")
     return y
 
 
@@ -69,8 +99,8 @@ def moe_grouped_matmul_dx(dy, W, offsets, rows=None, dx=None, ws=None):
         dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
     _is(dx, shape, dy.dtype, "dx")
     ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, dy.device)
-    check(lib().moe_grouped_matmul_dx(*sizes, _p(dy), _p(W), _p(offsets), _p(rows), _p(dx), _p(ws),
-                                      ws.numel(), _stream()), "moe_grouped_matmul_dx")
+    check(lib().moe_grouped_matmul_dx(*sizes, *_ptrs(dy, W, offsets, rows, dx, ws), ws.numel(),
+                                      _stream()), "moe_grouped_matmul_dx")
     return dx
 
 
@@ -91,9 +121,9 @@ def moe_grouped_matmul_dw(dy, x, offsets, rows=None, add=None, dW=None, out_dtyp
     _is(dW, shape, out_dtype, "dW")
     _is(add, shape, out_dtype, "add")
     ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, dy.device)
-    check(lib().moe_grouped_matmul_dw(*sizes, _p(dy), _p(x), _p(offsets), _p(rows),
-                                      _code(dW, "dW"), _p(add), _p(dW), _p(ws), ws.numel(),
-                                      _stream()), "moe_grouped_matmul_dw")
+    check(lib().moe_grouped_matmul_dw(*sizes, *_ptrs(dy, x, offsets, rows), _code(dW, "dW"),
+                                      *_ptrs(add, dW, ws), ws.numel(), _stream()),
+          "moe_grouped_matmul_dw")
     return dW
 
 
@@ -102,7 +132,7 @@ def moe_combine_backward(cfg: MoeConfig, dy, Y_perm, gates, topk, pos, keep, off
     """Gradients of moe_combine: (dY_perm, dgates).  Padding rows of dY_perm are
     not written."""
     T, k, d, dt = cfg.T, cfg.k, cfg.d, _tdtype(cfg)
-    R = moe_perm_rows(cfg)
+    R = _rows(cfg)
     if dY_perm is None:
         dY_perm = torch.empty((R, d), dtype=dt, device=dy.device)
     if dgates is None:
@@ -116,8 +146,8 @@ def moe_combine_backward(cfg: MoeConfig, dy, Y_perm, gates, topk, pos, keep, off
                                   (keep, (T, k), torch.uint8, "keep"),
                                   (offsets, (cfg.E + 1,), torch.int32, "offsets")):
         _is(t, shape, dtype, what)
-    check(lib().moe_combine_backward(ctypes.byref(cfg), _p(dy), _p(Y_perm), _p(gates), _p(topk),
-                                     _p(pos), _p(keep), _p(offsets), _p(dY_perm), _p(dgates),
+    check(lib().moe_combine_backward(ctypes.byref(cfg), *_ptrs(dy, Y_perm, gates, topk, pos, keep,
+                                                               offsets, dY_perm, dgates),
                                      _stream()), "moe_combine_backward")
     return dY_perm, dgates
 
@@ -149,7 +179,7 @@ def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, 
     accumulate the weight gradients are added to what they hold."""
     E, d, F, T, S, Fs = cfg.E, cfg.d, cfg.d_ff, cfg.T, cfg.n_shared, cfg.d_ff_shared
     dt, dev = _tdtype(cfg), x_perm.device
-    R = moe_perm_rows(cfg)
+    R = _rows(cfg)
     swiglu = cfg.act == 1
     if accumulate and grads is None:
         raise ValueError("accumulate adds to the weight gradients in `grads`")
@@ -182,10 +212,11 @@ def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, 
         _is(t, shape, dtype, what)
     ws = _ws(moe_ffn_backward_workspace_size(cfg), ws, dev)
     check(lib().moe_expert_ffn_backward(
-        ctypes.byref(cfg), _p(x_perm), _p(offsets), _p(kept), _p(dY_perm), _p(W1), _p(W3), _p(W2),
-        _p(x), _p(dY_shared), _p(Ws1), _p(Ws3), _p(Ws2), _p(g.dx_perm), _p(g.dW1), _p(g.dW3),
-        _p(g.dW2), _p(g.dx_shared), _p(g.dWs1), _p(g.dWs3), _p(g.dWs2), _code(g.dW1, "dW1"),
-        int(bool(accumulate)), _p(ws), ws.numel(), _stream()), "moe_expert_ffn_backward")
+        ctypes.byref(cfg), *_ptrs(x_perm, offsets, kept, dY_perm, W1, W3, W2, x, dY_shared, Ws1,
+                                  Ws3, Ws2, g.dx_perm, g.dW1, g.dW3, g.dW2, g.dx_shared, g.dWs1,
+                                  g.dWs3, g.dWs2),
+        _code(g.dW1, "dW1"), int(bool(accumulate)), *_ptrs(ws), ws.numel(), _stream()),
+        "moe_expert_ffn_backward")
     return grads
 
 
@@ -206,8 +237,9 @@ def moe_orthogonalize(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), scale=1.0, e
     _is(U, G.shape, torch.bfloat16, "U")
     c = (ctypes.c_float * 3)(*coeffs)
     ws = _ws(moe_orthogonalize_workspace_size(E, m, n, steps), ws, G.device)
-    check(lib().moe_orthogonalize(_code(G, "G"), E, m, n, _p(G), int(steps), c, float(eps),
-                                  float(scale), _p(U), _p(ws), ws.numel(), _stream()),
+    g, u, w = _ptrs(G, U, ws)
+    check(lib().moe_orthogonalize(_code(G, "G"), E, m, n, g, int(steps), c, float(eps),
+                                  float(scale), u, w, ws.numel(), _stream()),
           "moe_orthogonalize")
     return U
 
