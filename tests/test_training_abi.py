@@ -53,7 +53,7 @@ def test_workspace_sizes():
     R = moe.moe_perm_rows(cfg)
     assert moe.moe_ffn_backward_workspace_size(cfg) >= 3 * 2 * (R * 192 + 2 * 100 * 64)
     assert moe.moe_ffn_backward_workspace_size(moe.moe_config(cfg, d_ff=100)) == 0
-    assert moe.moe_orthogonalize_workspace_size(3, 100, 50) >= 3 * 8 * (100 * 50 + 50 * 50)
+    assert moe.moe_orthogonalize_workspace_size(3, 100, 50) >= 3 * (8 * 100 * 50 + 4 * 50 * 50)
     for bad in ((0, 8, 8, 5), (1025, 8, 8, 5), (1, 0, 8, 5), (1, 8, 0, 5), (1, 8, 8, 0),
                 (1, 8, 8, 33), (1, (1 << 20) + 1, 8, 5)):
         assert moe.moe_orthogonalize_workspace_size(*bad) == 0
