@@ -17,16 +17,21 @@ enum Mode { RAGGED_M = 0, RAGGED_K = 1, DENSE = 2 };
 
 constexpr int kSets = 6;
 constexpr int kEntries = 1024;   // (set, group) pairs of a launch
+// Scratch of cut tiles: the parts, and the counters (most tiles cut at a time:
+// as many as parts fit, at least two parts each).
+constexpr int kPartialBytes = 32 << 20;
+constexpr int kCounterBytes = kPartialBytes / (128 * 128 * 4) / 2 * 8 * 8;
 
 // One family of products of a launch: out[g] = sum over K segments of A B^T.
 struct Set {
     // Segment i of a tile's contraction multiplies operand pair i % period; with
     // seg_grouped both operands' group is i / period.
     CUtensorMap a[2], b[2];
+    CUtensorMap a_few;           // a[0] in boxes of 32 rows, if has_few (ONE_128, one segment)
     CUtensorMap b3;              // EPI_SWIGLU: W3 (b[0] = W1, b[1] = W2)
     int mode, groups, ent0;      // ent0: first entry of the tile table
     int M, N, K;                 // output rows (not RAGGED_M), columns, contraction (not RAGGED_K)
-    int segs, period, seg_grouped;
+    int segs, period, seg_grouped, has_few;
     int a_grouped, b_grouped;    // 1: the operand has one matrix per group
     int sym;                     // 1: out is symmetric; only tiles on or below the diagonal
     int ld;                      // row pitch of out (elements)
@@ -53,6 +58,12 @@ struct __align__(64) Params {
     const int32_t *rows;         // [G], nullable: offsets[g + 1] - offsets[g]
     int n_rows;                  // rows of the tall buffers; the table is held inside them
     int fp16;                    // operands are fp16 (else bf16)
+    // scratch of tiles cut along their contraction: parts' accumulators, and a
+    // counter for each warp of each cut tile (any contents).  NULL: no tile is cut
+    float *partial;
+    unsigned long long *counters;
+    int partial_bytes;
+    unsigned long long tag;      // of this launch in the counters
     int32_t *status;
     int clear_status;
     unsigned long long timeout_ns;
@@ -77,8 +88,11 @@ enum Epi { EPI_ROWS = 0, EPI_DW = 1, EPI_NS = 2, EPI_GELU = 3, EPI_SWIGLU = 4 };
 // matrix (its other index is contiguous), K = the contraction is contiguous.
 enum Layout { A_K_B_K = 0, A_K_B_MN = 1, A_MN_B_MN = 2 };
 
-// Launches with `pair` 1 for 256-row SM-pair tiles, 0 for 128-row tiles.
-cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t s);
+// PAIR_256: 256 x 256 on SM pairs (hidden gradients: 256 x 128); ONE_128: 128 x
+// 128 and ONE_32: 32 x 128 (EPI_ROWS alone) on single SMs.
+enum Tiles { PAIR_256, ONE_128, ONE_32 };
+
+cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s);
 
 // Maps of a [groups, rows, cols] 2-byte tensor with row pitch ld for the
 // operand's role (group_stride in elements).
@@ -87,8 +101,8 @@ bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t
 bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
             int64_t groups, int64_t group_stride, int box_rows);
 // Box rows of a K-major B, and of an MN-major operand, in launches of this shape.
-int b_box_rows(Epi epi, bool pair);
-int mn_box_rows(Epi epi, bool pair);
+int b_box_rows(Epi epi, Tiles tiles);
+int mn_box_rows(Epi epi, Tiles tiles);
 
 }  // namespace grp
 }  // namespace moe

@@ -14,14 +14,23 @@
 // Ragged contractions (dW): a group's rows end anywhere, and what follows
 // belongs to the next group or to nobody (it may hold NaN, so it cannot be
 // multiplied by zeros).  The MMA stops at the 16-row step holding the last
-// row; the producer waits for that box and clears the up to 15 rows behind it
-// in shared memory before handing the stage over.
+// row; a warp of its own waits for that stage's copies and clears the up to 15
+// rows behind it in shared memory before handing the stage over, while the
+// loads go on to the next tile (5.3 us a tile of two rows when the loading warp
+// did it in turn).
 //
 // The tensor cores truncate when they add to an fp32 accumulator, a bias of
 // about 2e-8 of the sum for every 16 rows (measured: 1.6e-6 after 1536 rows,
 // where fp32 rounding alone leaves 3e-7), so a weight gradient over many rows
 // is summed in accumulators of 512 rows each, which the epilogue adds up in
 // registers (round to nearest) while the next one fills: 128 values a thread.
+//
+// Work is dealt as tiles, one to each CTA (pair) in turn.  Where the last round
+// would leave most of them idle (or, with few rows, every round), the tiles of
+// the last rounds are cut along the contraction: each part leaves its fp32
+// accumulators in the workspace, and the warp that finishes a tile's part last
+// adds the parts up in their order and stores the rows, so the result does not
+// depend on who was last.  split_plan() weighs the rounds saved against that.
 //
 // Output rows go from registers to memory, each masked by the group's end: rows
 // behind it are neither written nor read.
@@ -35,6 +44,9 @@
 
 #include <cuda_fp16.h>
 #include <string.h>
+#include <time.h>
+
+#include <atomic>
 
 namespace moe {
 namespace grp {
@@ -44,16 +56,20 @@ using namespace tc;
 namespace {
 
 constexpr int EPI_WARPS = 8;
-constexpr int A_BYTES = 128 * 128;       // 128 rows x 64 elements of one CTA
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int RING_BYTES = 192 * 1024;
 
-template <int CTAS, int BN, int EPI>
+// AR: rows of A a CTA takes, 128, or 32 for groups of few rows: the MMA's other
+// rows read on into the next bytes of the ring, their results are never stored,
+// and the ring holds 5 x 32 KB of weights instead of 3 x 32.
+template <int CTAS, int BN, int EPI, int AR>
 struct Shape {
     static constexpr bool ACT = EPI == EPI_GELU || EPI == EPI_SWIGLU;
-    static constexpr int BM = 128 * CTAS;
-    static constexpr int FIRST_EPI = 2;   // first of the epilogue warps
+    static constexpr int BM = AR * CTAS;
+    static constexpr int A_BYTES = AR * 128;             // AR rows x 64 elements
+    static constexpr int FIRST_EPI = EPI == EPI_DW ? 3 : 2;   // first of the epilogue warps
     static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
+    static constexpr int MMA_M = 128 * CTAS;
     // accumulator columns of the widest B tile (ACT: u, with v beside it)
     static constexpr int BNB = EPI == EPI_SWIGLU ? 2 * BN : BN;
     static constexpr int B_ROWS = BNB / CTAS;            // B rows of one CTA
@@ -61,13 +77,13 @@ struct Shape {
     static constexpr int SUB = A_BYTES + B_BYTES;
     // 128 of K a stage where three stages fit: half the barrier round trips
     static constexpr int KSUB = 6 * SUB <= RING_BYTES ? 2 : 1;
-    static constexpr int STAGES = RING_BYTES / (KSUB * SUB) > 6 ? 6 : RING_BYTES / (KSUB * SUB);
+    static constexpr int STAGES = AR < 128 ? 5 : RING_BYTES / (KSUB * SUB);
     static constexpr int BK = 64 * KSUB;
     static constexpr int MN_BLOCK = BK * 128;            // 64 columns of an MN-major stage
     static constexpr int OFF_B = STAGES * KSUB * A_BYTES;
     static constexpr int OFF_BAR = OFF_B + STAGES * KSUB * B_BYTES;
     static constexpr int OFF_TAB = OFF_BAR + 256;
-    static constexpr int SMEM = OFF_TAB + 4 * (kEntries + 1) + 8 * kMaxE + 1024;   // + alignment slack
+    static constexpr int SMEM = OFF_TAB + 8 * kMaxE + 4 * (kEntries + 4) + 1024;   // + alignment slack
     // EPI_DW: contraction rows summed in one accumulator before the epilogue
     // adds it, in registers, to the tile's running sum (0: all of them)
     static constexpr int CHUNK = EPI == EPI_DW ? 512 : 0;
@@ -82,6 +98,16 @@ struct Tile {
     int mg;            // output rows of the group
     int row0;          // first row of the group in the tall buffers (RAGGED_M)
     int k0, klen;      // contraction: first index and length
+    int kbs;           // its blocks of BK, for one segment
+    int b0, b1;        // the blocks of this part, over all segments
+    int part, parts;   // which of how many parts of a tile
+    int cut;           // number among the cut tiles
+};
+
+// The first `whole` tiles are items by themselves; every later one is `parts`
+// items, one for each part of its contraction.
+struct Plan {
+    int whole, parts, items;
 };
 
 // Tiles of entry (set, g).
@@ -98,9 +124,57 @@ __device__ __forceinline__ int entry_tiles(const Set &s, const int2 *span, int g
     return n;
 }
 
-template <int BM, int BN>
-__device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const int2 *span, int tile)
+// A plan for `tiles` tiles of `kb` contraction blocks each on `units` CTAs or
+// pairs, `most` cut items at most.  Costs in blocks (0.8 us): an item's epilogue
+// 2; a cut tile 3 to leave and 3.5 a part to add up.  Lane i of a warp tries i parts
+// for the tiles of the last round, or of the last two, or for all.
+template <int CTAS>
+__device__ __forceinline__ Plan split_plan(int tiles, int kb, int units, int most, int lane)
 {
+    const int rounds = tiles / units;
+    const int parts = 1 + (lane & 15);
+    float best = 1e30f;
+    int whole = tiles;
+    if (lane == 0) {
+        best = (float)((tiles + units - 1) / units) * (kb + 2);
+    } else if (parts > 1 && 2 * parts <= kb) {
+        // lanes 1..15: tiles past the last full round; 17..31: one round more
+        const int full = lane < 16 ? rounds : rounds - 1;
+        const int cut = tiles - full * units;
+        if (full >= 0 && cut > 0 && (int64_t)cut * parts <= most) {
+            best = (float)full * (kb + 2) +
+                   (float)((cut * parts + units - 1) / units) * ((kb + parts - 1) / parts + 2) + 3 +
+                   3.5f * parts;
+            whole = full * units;
+        }
+    }
+    float low = best;
+#pragma unroll
+    for (int s = 16; s; s >>= 1)
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, s));
+    const int from = __ffs(__ballot_sync(0xffffffffu, best == low)) - 1;
+    Plan pl;
+    pl.whole = __shfl_sync(0xffffffffu, whole, from);
+    pl.parts = __shfl_sync(0xffffffffu, parts, from);
+    pl.items = pl.whole + (tiles - pl.whole) * pl.parts;
+    return pl;
+}
+
+template <int BM, int BN, int BK>
+__device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const int2 *span,
+                                       const Plan &pl, int item)
+{
+    Tile t;
+    int tile = item;
+    t.part = 0;
+    t.parts = 1;
+    t.cut = 0;
+    if (item >= pl.whole) {
+        t.cut = (item - pl.whole) / pl.parts;
+        t.part = (item - pl.whole) % pl.parts;
+        t.parts = pl.parts;
+        tile = pl.whole + t.cut;
+    }
     int lo = 0, hi = p.entries;   // last entry with tstart <= tile
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -109,7 +183,6 @@ __device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const
         else
             hi = mid;
     }
-    Tile t;
     int set = 0;
     while (set + 1 < p.nsets && p.set[set + 1].ent0 <= lo)
         ++set;
@@ -124,6 +197,10 @@ __device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const
         t.row0 = span[t.g].x, t.mg = span[t.g].y;
     else if (s.mode == RAGGED_K)
         t.k0 = span[t.g].x, t.klen = span[t.g].y;
+    t.kbs = (t.klen + BK - 1) / BK;
+    const int blocks = t.kbs * s.segs;
+    t.b0 = blocks * t.part / t.parts;
+    t.b1 = blocks * (t.part + 1) / t.parts;
     int i = tile - tstart[lo];
     const int nt = (s.N + BN - 1) / BN;
     if (s.sym) {
@@ -142,6 +219,14 @@ __device__ __forceinline__ Tile decode(const Params &p, const int *tstart, const
         t.n0 = (i / mt) * BN;
     }
     return t;
+}
+
+// Whether a contraction's last block of `rem` rows ends inside a 16-row step,
+// so that rows behind it have to be cleared.
+template <int BK>
+__device__ __forceinline__ bool ragged_tail(int rem)
+{
+    return rem < BK && (rem & 15);
 }
 
 // MN-major operand, 128-byte swizzle: 64 contiguous elements per 128-byte row,
@@ -300,6 +385,52 @@ __device__ __forceinline__ void store_row(uint8_t *p, int end, int bytes, const 
     }
 }
 
+// This warp's part of a cut tile is written; true for the last of the parts,
+// which then sees them all.  The counter's upper 48 bits are the launch's tag:
+// any other tag there (what the memory held before) counts as zero, so nothing
+// has to be cleared first.
+__device__ __forceinline__ bool last_part(unsigned long long *count, unsigned long long tag,
+                                          int parts, int lane)
+{
+    __threadfence();
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) {
+        unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(count), now;
+        for (;;) {   // one of at most 16 parts: some other part got through on every failure
+            const unsigned long long n = (seen >> 16 == tag ? seen & 0xffff : 0) + 1;
+            last = n == (unsigned long long)parts;
+            now = atomicCAS(count, seen, last ? 0 : tag << 16 | n);
+            if (now == seen)
+                break;
+            seen = now;
+        }
+    }
+    last = __shfl_sync(0xffffffffu, last, 0);
+    __threadfence();
+    return last;
+}
+
+// 32 columns of a cut tile's row, its parts added in their order.
+__device__ __forceinline__ void add_parts(const float4 *from, int64_t step, int parts, float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        v[j] = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < parts; ++k, from += step) {
+        float4 f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = __ldcg(from + 32 * j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[4 * j] += f[j].x, v[4 * j + 1] += f[j].y;
+            v[4 * j + 2] += f[j].z, v[4 * j + 3] += f[j].w;
+        }
+    }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -352,13 +483,13 @@ __device__ __forceinline__ void store_mirror(const uint32_t *w, uint16_t *out, i
     }
 }
 
-template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
+template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI, int AR>
+__global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     grouped_kernel(const __grid_constant__ Params p)
 {
-    using S = Shape<CTAS, BN, EPI>;
+    using S = Shape<CTAS, BN, EPI, AR>;
     constexpr bool ACT = S::ACT;
-    constexpr int STAGES = S::STAGES, KSUB = S::KSUB, BM = S::BM;
+    constexpr int STAGES = S::STAGES, KSUB = S::KSUB, BM = S::BM, A_BYTES = S::A_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -370,11 +501,12 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-    const uint32_t tail_bar = bar0 + 8u * (2 * STAGES + 5);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + 8 * (2 * STAGES + 6));
+    auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + 8 * (3 * STAGES + 5));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int2 *span = reinterpret_cast<int2 *>(smem + S::OFF_TAB);   // [groups] first row, rows
     int *tstart = reinterpret_cast<int *>(span + kMaxE);        // [entries + 1]
+    int *plan_slot = tstart + kEntries + 1;                     // the Plan
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
@@ -386,13 +518,13 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), CTAS);   // each CTA's producer, with its bytes
             mbar_init(empty_bar(s), 1);
+            mbar_init(tail_bar(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
             mbar_init(tempty_bar(a), CTAS * EPI_WARPS);
         }
         mbar_init(drain_bar, 1);
-        mbar_init(tail_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -442,8 +574,27 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                 tstart[e] = base + sum - n;
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (lane == 0)
+        Plan pl{base, 1, base};
+        if (p.partial && base > 0) {
+            // contraction blocks of a tile, averaged over the first set's groups
+            const Set &s = p.set[0];
+            int k = s.K;
+            if (s.mode == RAGGED_K) {
+                k = 0;
+                for (int g = lane; g < s.groups; g += 32)
+                    k += span[g].y;
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    k += __shfl_xor_sync(0xffffffffu, k, d);
+                k /= s.groups;
+            }
+            pl = split_plan<CTAS>(base, s.segs * ((k + S::BK - 1) / S::BK), units,
+                                  p.partial_bytes / (BM * BN * 4), lane);
+        }
+        if (lane == 0) {
             tstart[p.entries] = base;
+            plan_slot[0] = pl.whole, plan_slot[1] = pl.parts, plan_slot[2] = pl.items;
+        }
     }
     tc_fence_before();
     if (CTAS == 2)
@@ -451,26 +602,27 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
     else
         __syncthreads();
     tc_fence_after();
-    const int total = tstart[p.entries];
+    const Plan pl{plan_slot[0], plan_slot[1], plan_slot[2]};
+    const int total = pl.items;
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp == 0) {
         // ================= loads (both CTAs) =================
         int stage = 0;
-        uint32_t phase = 0, tail_phase = 0;
+        uint32_t phase = 0;
         int issued = 0;
         uint32_t last_phase = 0;   // bit s: phase of stage s's last use
         bool ok = true;
         Tile next;
         if (unit < total)
-            next = decode<BM, BN>(p, tstart, span, unit);
+            next = decode<BM, BN, S::BK>(p, tstart, span, pl, unit);
         for (int tile = unit; ok && tile < total; tile += units) {
             const Tile t = next;
             bool ahead = false;   // the next tile is looked up behind this one's first stage
             const Set &s = p.set[t.set];
-            const int m_row = t.m0 + (int)rank * 128 + (s.mode == RAGGED_M ? t.row0 : 0);
-            const int segs = ACT ? 2 : s.segs;
-            for (int sg = 0; ok && sg < segs; ++sg) {
+            const int m_row = t.m0 + (int)rank * AR + (s.mode == RAGGED_M ? t.row0 : 0);
+            int sg = t.kbs > 0 ? t.b0 / t.kbs : 0, kb = t.b0 - sg * t.kbs;
+            while (ok && sg * t.kbs + kb < t.b1) {
                 const int ph = ACT ? sg : sg % s.period;
                 const int bi = ACT ? 1 - sg : ph;
                 const int grp = !ACT && s.seg_grouped ? sg / s.period : t.g;
@@ -480,9 +632,15 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                 // B rows of this CTA, and their first
                 const int b_rows = ACT ? (uv ? S::B_ROWS : BN / CTAS) : S::B_ROWS;
                 const int b_row = t.n0 + (uv && CTAS == 2 ? 0 : (int)rank * (BN / CTAS));
-                const CUtensorMap *am = &s.a[ph];
+                // a tile of few rows loads them in boxes of 32 (the MMA's other rows
+                // are whatever the stage holds; they are never stored)
+                const bool few = EPI == EPI_ROWS && s.has_few && t.mg - t.m0 <= 96;
+                const int a_box = few ? 32 : AR;
+                const int a_rows = few ? (t.mg - t.m0 + 31) / 32 * 32 : AR;
+                const CUtensorMap *am = few ? &s.a_few : &s.a[ph];
                 const CUtensorMap *bm = uv && rank == 1 ? &s.b3 : &s.b[bi];
-                for (int kb = 0; kb * S::BK < t.klen; ++kb) {
+                const int end = min(t.kbs, t.b1 - sg * t.kbs);
+                for (; kb < end; ++kb) {
                     int okw = lane == 0 ? (wait_bar(empty_bar(stage), phase ^ 1u, ctl) ? 1 : 0) : 1;
                     if (!__shfl_sync(0xffffffffu, okw, 0)) {
                         ok = false;
@@ -492,7 +650,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     const int nks = rem >= S::BK ? KSUB : (rem + 63) / 64;
                     // K-major: nks boxes of 64 of K; MN-major: one box of BK per 64 columns
                     const uint32_t bytes =
-                        (uint32_t)((A_MN ? KSUB : nks) * A_BYTES +
+                        (uint32_t)((A_MN ? KSUB : nks) * a_rows * 128 +
                                    (b_mn ? KSUB : nks) * b_rows * 128);
                     const uint32_t fb = CTAS == 2 ? map_to_rank(full_bar(stage), 0)
                                                   : full_bar(stage);
@@ -500,16 +658,16 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     const uint32_t sb = sB + stage * KSUB * S::B_BYTES;
                     const int kc = t.k0 + kb * S::BK;
                     // rows behind the group's last must be cleared before use
-                    const bool tail = A_MN && s.mode == RAGGED_K && rem < S::BK && (rem & 15);
+                    const bool tail = EPI == EPI_DW && s.mode == RAGGED_K && ragged_tail<S::BK>(rem);
                     if (lane == 0) {
                         if (tail)
-                            mbar_expect_tx(tail_bar, bytes);
+                            mbar_expect_tx(tail_bar(stage), bytes);
                         else
                             arrive_bytes<CTAS>(fb, bytes);
                         auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1,
                                         int c2) {
-                            if (A_MN && tail)
-                                tma_load_3d(dst, m, tail_bar, c0, c1, c2);
+                            if (EPI == EPI_DW && tail)
+                                tma_load_3d(dst, m, tail_bar(stage), c0, c1, c2);
                             else
                                 load_box<CTAS>(dst, m, fb, c0, c1, c2);
                         };
@@ -518,7 +676,9 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                             load(sa + S::MN_BLOCK, am, m_row + 64, kc, ga);
                         } else {
                             for (int ks = 0; ks < nks; ++ks)
-                                load(sa + ks * A_BYTES, am, kc + ks * 64, m_row, ga);
+                                for (int r = 0; r < a_rows; r += a_box)
+                                    load(sa + ks * A_BYTES + r * 128, am, kc + ks * 64, m_row + r,
+                                         ga);
                         }
                         if (b_mn) {
                             for (int b = 0; b < b_rows / 64; ++b)
@@ -532,32 +692,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                             }
                         }
                     }
-                    if (tail) {
-                        okw = lane == 0 ? (wait_bar(tail_bar, tail_phase, ctl, false) ? 1 : 0) : 1;
-                        okw = __shfl_sync(0xffffffffu, okw, 0);
-                        tail_phase ^= 1u;
-                        const int n = (16 - (rem & 15)) * 8;   // 16-byte pieces per 64 columns
-                        const int boxes = 2 + b_rows / 64;
-                        for (int i = lane; i < n * boxes; i += 32) {
-                            const int box = i / n;
-                            const uint32_t dst = (box < 2 ? sa + box * S::MN_BLOCK
-                                                          : sb + (box - 2) * S::MN_BLOCK) +
-                                                 rem * 128 + (i % n) * 16;
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst),
-                                         "r"(0)
-                                         : "memory");
-                        }
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            arrive_written<CTAS>(fb);
-                        if (!okw) {
-                            ok = false;
-                            break;
-                        }
-                    }
                     if (!ahead && tile + units < total)
-                        next = decode<BM, BN>(p, tstart, span, tile + units);
+                        next = decode<BM, BN, S::BK>(p, tstart, span, pl, tile + units);
                     ahead = true;
                     issued |= 1 << stage;
                     last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
@@ -566,9 +702,11 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                         phase ^= 1u;
                     }
                 }
+                ++sg;
+                kb = 0;
             }
             if (!ahead && tile + units < total)   // an empty contraction
-                next = decode<BM, BN>(p, tstart, span, tile + units);
+                next = decode<BM, BN, S::BK>(p, tstart, span, pl, tile + units);
         }
         // the leader's full barriers count both CTAs' bytes: drain there
         if (leader && lane == 0)
@@ -579,14 +717,14 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
         // ================= MMA issue (leader CTA only) =================
         if (lane == 0 && leader) {
             const uint32_t fmt = p.fp16 ? 0u : (1u << 7) | (1u << 10);
-            const uint32_t idesc0 = (1u << 4) | fmt | ((uint32_t)(BM >> 4) << 24);
+            const uint32_t idesc0 = (1u << 4) | fmt | ((uint32_t)(S::MMA_M >> 4) << 24);
             int stage = 0;
             uint32_t phase = 0;
             int it = 0;
             bool ok = true, any = false;
             Tile next;
             if (unit < total)
-                next = decode<BM, BN>(p, tstart, span, unit);
+                next = decode<BM, BN, S::BK>(p, tstart, span, pl, unit);
             for (int tile = unit; ok && tile < total; tile += units, ++it) {
                 const Tile t = next;
                 bool ahead = false;
@@ -597,9 +735,9 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const int segs = ACT ? 2 : s.segs;
                 bool first = true;
-                for (int sg = 0; ok && sg < segs; ++sg) {
+                int sg = t.kbs > 0 ? t.b0 / t.kbs : 0, kb = t.b0 - sg * t.kbs, n = 0;
+                while (ok && sg * t.kbs + kb < t.b1) {
                     const bool uv = EPI == EPI_SWIGLU && sg == 1;
                     const bool b_mn = ACT ? sg == 0 : B_MN;
                     uint32_t d = tmem_base;
@@ -622,8 +760,9 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     const uint32_t idesc = idesc0 | (A_MN ? 1u << 15 : 0u) |
                                            (b_mn ? 1u << 16 : 0u) |
                                            ((uint32_t)((uv ? 2 * BN : BN) >> 3) << 17);
-                    for (int kb = 0; kb * S::BK < t.klen; ++kb) {
-                        if (S::CHUNK > 0 && kb > 0 && kb % (S::CHUNK > 0 ? S::CHUNK / S::BK : 1) == 0) {
+                    const int end = min(t.kbs, t.b1 - sg * t.kbs);
+                    for (; kb < end; ++kb, ++n) {
+                        if (S::CHUNK > 0 && n > 0 && n % (S::CHUNK > 0 ? S::CHUNK / S::BK : 1) == 0) {
                             // this accumulator is full: on to the other one
                             commit_all<CTAS>(tfull_bar(slot));
                             ++it;
@@ -665,18 +804,20 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                         commit_all<CTAS>(empty_bar(stage));
                         any = true;
                         if (!ahead && tile + units < total)
-                            next = decode<BM, BN>(p, tstart, span, tile + units);
+                            next = decode<BM, BN, S::BK>(p, tstart, span, pl, tile + units);
                         ahead = true;
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
+                    ++sg;
+                    kb = 0;
                 }
                 if (!ok)
                     break;
                 if (!ahead && tile + units < total)   // an empty contraction
-                    next = decode<BM, BN>(p, tstart, span, tile + units);
+                    next = decode<BM, BN, S::BK>(p, tstart, span, pl, tile + units);
                 commit_all<CTAS>(tfull_bar(slot));
                 any = true;
             }
@@ -688,16 +829,53 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                 wait_bar(drain_bar, 0, ctl, false);
             }
         }
+    } else if (EPI == EPI_DW && warp == 2) {
+        // ================= ragged tails (both CTAs) =================
+        int blocks = 0;          // stages used by the tiles before
+        uint32_t parity = 0;     // bit s: phase of stage s's next tail
+        bool ok = true;
+        for (int tile = unit; ok && tile < total; tile += units) {
+            const Tile t = decode<BM, BN, S::BK>(p, tstart, span, pl, tile);
+            const int rem = t.klen - (t.kbs - 1) * S::BK;
+            blocks += t.b1 - t.b0;
+            if (p.set[t.set].mode != RAGGED_K || t.b1 == t.b0 || t.b1 != t.kbs ||
+                !ragged_tail<S::BK>(rem))
+                continue;
+            const int stage = (blocks - 1) % STAGES;
+            ok = wait_bar(tail_bar(stage), parity >> stage & 1, ctl);
+            ok = __all_sync(0xffffffffu, ok);
+            parity ^= 1u << stage;
+            // 128 bytes a row, so 8 lanes a row: four rows of a box at a time
+            const uint32_t at = (uint32_t)(rem + (lane >> 3)) * 128 + (lane & 7) * 16;
+            const int rows = 16 - (rem & 15);
+            for (int box = 0; box < 2 + S::B_ROWS / 64; ++box) {
+                const uint32_t dst = box < 2 ? sA + stage * KSUB * A_BYTES + box * S::MN_BLOCK
+                                             : sB + stage * KSUB * S::B_BYTES +
+                                                   (box - 2) * S::MN_BLOCK;
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    if (r + (lane >> 3) < rows)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at +
+                                                                                       r * 128),
+                                     "r"(0)
+                                     : "memory");
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                arrive_written<CTAS>(CTAS == 2 ? map_to_rank(full_bar(stage), 0) : full_bar(stage));
+        }
     } else if (warp >= S::FIRST_EPI) {
         // ================= epilogue (eight warps, both CTAs) =================
         const int q = warp & 3, half = (warp - S::FIRST_EPI) >> 2;
         int it = 0;
         for (int tile = unit; tile < total; tile += units, ++it) {
-            const Tile t = decode<BM, BN>(p, tstart, span, tile);
+            const Tile t = decode<BM, BN, S::BK>(p, tstart, span, pl, tile);
             const Set &s = p.set[t.set];
             int slot = it & 1;
             const int m = t.m0 + (int)rank * 128 + q * 32;   // first row, in the group
-            const int rv = t.mg - m;                          // rows of it from there on
+            // rows of it from there on, in this tile
+            const int rv = AR < 128 && q > 0 ? 0 : t.mg - m;
             const int c_end = rv > 0 ? min((half + 1) * (BN / 2), s.N - t.n0) : 0;
             // base is read a chunk ahead: the first before the products are done
             uint32_t bhi[EPI == EPI_NS ? 16 : 1], blo[EPI == EPI_NS ? 16 : 1];
@@ -718,9 +896,17 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                                 row * s.ld + t.n0;
             const bool mine = lane < rv;
             const int bytes = s.bytes;
+            // a cut tile's parts: 32 rows x BN / 2 columns of this warp, 4 columns of
+            // a lane together
+            const int wid = (int)rank * EPI_WARPS + half * 4 + q;
+            const int64_t part_step = (int64_t)CTAS * EPI_WARPS * (BN / 8) * 32;
+            float4 *part0 = reinterpret_cast<float4 *>(p.partial) +
+                            ((int64_t)t.cut * t.parts + t.part) * part_step +
+                            (int64_t)wid * (BN / 8) * 32;
+            unsigned long long *count = p.counters + t.cut * (CTAS * EPI_WARPS) + wid;
             if constexpr (EPI == EPI_DW) {
                 float sum[BN / 2];
-                if (t.klen == 0) {   // nothing was accumulated: an empty group's sum
+                if (t.b0 == t.b1) {   // nothing was accumulated: an empty group's sum
 #pragma unroll
                     for (int i = 0; i < BN / 2; ++i)
                         sum[i] = 0.f;
@@ -730,7 +916,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                         tmem_ld32(tq + slot * BN + half * (BN / 2) + 32 * i, sum + 32 * i);
                 }
                 bool ok = true;
-                for (int k = S::CHUNK; k < t.klen; k += S::CHUNK) {
+                for (int k = S::CHUNK / S::BK; k < t.b1 - t.b0; k += S::CHUNK / S::BK) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -764,6 +950,21 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                         mbar_arrive_remote(map_to_rank(tempty_bar(slot), 0));
                     else
                         mbar_arrive(tempty_bar(slot));
+                }
+                if (t.parts > 1) {
+                    if (rv <= 0)
+                        continue;
+                    float4 *at = part0 + lane;
+#pragma unroll
+                    for (int i = 0; i < BN / 8; ++i)
+                        at[32 * i] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2],
+                                                 sum[4 * i + 3]);
+                    if (!last_part(count, p.tag, t.parts, lane))
+                        continue;
+                    const float4 *from = part0 + lane - t.part * part_step;
+#pragma unroll
+                    for (int i = 0; i < BN / 2; i += 32)
+                        add_parts(from + 8 * i, part_step, t.parts, sum + i);
                 }
                 if (mine) {
                     const int c0 = half * (BN / 2), cols = c_end - c0;
@@ -807,6 +1008,34 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     }
                 }
                 continue;
+            }
+            bool released = false;
+            auto release = [&]() {   // this warp is done with the accumulator
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CTAS == 2)
+                        mbar_arrive_remote(map_to_rank(tempty_bar(slot), 0));
+                    else
+                        mbar_arrive(tempty_bar(slot));
+                }
+            };
+            if (!ACT && t.parts > 1) {
+                if (rv > 0) {
+#pragma unroll
+                    for (int i = 0; i < BN / 64; ++i) {
+                        float v[32];
+                        tmem_ld32(tq + slot * BN + half * (BN / 2) + 32 * i, v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            part0[(8 * i + j) * 32 + lane] =
+                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                }
+                release();
+                released = true;
+                if (rv <= 0 || !last_part(count, p.tag, t.parts, lane))
+                    continue;
             }
 #pragma unroll 1
             for (int c = half * (BN / 2); c < c_end; c += 32) {
@@ -872,7 +1101,12 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                         }
                     }
                 } else {
-                    tmem_ld32(tq + slot * BN + c, v);
+                    if (t.parts > 1) {
+                        add_parts(part0 + lane - t.part * part_step + (c - half * (BN / 2)) * 8,
+                                  part_step, t.parts, v);
+                    } else {
+                        tmem_ld32(tq + slot * BN + c, v);
+                    }
                     if constexpr (EPI == EPI_ROWS) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -938,14 +1172,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CTAS == 2)
-                    mbar_arrive_remote(map_to_rank(tempty_bar(slot), 0));
-                else
-                    mbar_arrive(tempty_bar(slot));
-            }
+            if (!released)
+                release();
         }
     }
 
@@ -967,15 +1195,15 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI>::THREADS, 1)
     }
 }
 
-template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI>
+template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI, int AR = 128>
 cudaError_t launch_one(const Params &p, cudaStream_t s)
 {
-    using S = Shape<CTAS, BN, EPI>;
+    using S = Shape<CTAS, BN, EPI, AR>;
     static_assert(S::SMEM <= 232448, "shared memory");
     // mn_box_rows: the rows of a stage
-    static_assert(S::BK == (EPI == EPI_SWIGLU && CTAS == 1 ? 64 : 128), "stage");
+    static_assert(S::BK == (CTAS == 1 && EPI == EPI_SWIGLU ? 64 : 128), "stage");
     static_assert(S::DH_COL + 2 * BN <= 512 || !S::ACT, "TMEM");
-    auto kern = grouped_kernel<CTAS, BN, A_MN, B_MN, EPI>;
+    auto kern = grouped_kernel<CTAS, BN, A_MN, B_MN, EPI, AR>;
     cudaError_t err = raise_smem_limit((const void *)kern, S::SMEM);
     if (err != cudaSuccess)
         return err;
@@ -1005,7 +1233,7 @@ cudaError_t launch_one(const Params &p, cudaStream_t s)
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-constexpr int kBnPair = 256, kBnOne = 128, kBnAct = 128;
+constexpr int kBnAct = 128;
 
 }  // namespace
 
@@ -1023,18 +1251,14 @@ bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-int b_box_rows(Epi epi, bool pair)
+int b_box_rows(Epi epi, Tiles tiles)   // SwiGLU: a box of W1 and one of W3
 {
-    if (epi == EPI_SWIGLU)
-        return kBnAct;   // W1 and W3 boxes of BN rows each
-    if (epi == EPI_GELU)
-        return pair ? kBnAct / 2 : kBnAct;
-    return pair ? kBnPair / 2 : kBnOne;
+    return epi == EPI_GELU && tiles == PAIR_256 ? kBnAct / 2 : 128;
 }
 
-int mn_box_rows(Epi epi, bool pair) { return epi == EPI_SWIGLU && !pair ? 64 : 128; }
+int mn_box_rows(Epi epi, Tiles tiles) { return epi == EPI_SWIGLU && tiles != PAIR_256 ? 64 : 128; }
 
-cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t s)
+cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s)
 {
     int ents = 0;
     for (int i = 0; i < p.nsets; ++i) {
@@ -1057,7 +1281,12 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t
     if (ents > kEntries)
         return cudaErrorInvalidValue;
     p.entries = ents;
+    if (epi == EPI_GELU || epi == EPI_SWIGLU)
+        p.partial = nullptr;   // u, v and dh are not cut
     p.timeout_ns = 2000000000ull;
+    static std::atomic<unsigned long long> calls{(unsigned long long)time(nullptr) << 20};
+    p.tag = (calls.fetch_add(1) * 0x9E3779B97F4A7C15ull) >> 16 | 1;
+    const bool pair = tiles == PAIR_256;
     switch (epi) {
     case EPI_GELU:
         return pair ? launch_one<2, kBnAct, false, false, EPI_GELU>(p, s)
@@ -1066,23 +1295,26 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, bool pair, cudaStream_t
         return pair ? launch_one<2, kBnAct, false, false, EPI_SWIGLU>(p, s)
                     : launch_one<1, kBnAct, false, false, EPI_SWIGLU>(p, s);
     case EPI_DW:
-        return pair ? launch_one<2, kBnPair, true, true, EPI_DW>(p, s)
-                    : launch_one<1, kBnOne, true, true, EPI_DW>(p, s);
+        return pair ? launch_one<2, 256, true, true, EPI_DW>(p, s)
+                    : launch_one<1, 128, true, true, EPI_DW>(p, s);
     case EPI_ROWS:
+        if (tiles == ONE_32)
+            return layout == A_K_B_MN ? launch_one<1, 128, false, true, EPI_ROWS, 32>(p, s)
+                                      : launch_one<1, 128, false, false, EPI_ROWS, 32>(p, s);
         if (layout == A_K_B_MN)
-            return pair ? launch_one<2, kBnPair, false, true, EPI_ROWS>(p, s)
-                        : launch_one<1, kBnOne, false, true, EPI_ROWS>(p, s);
-        return pair ? launch_one<2, kBnPair, false, false, EPI_ROWS>(p, s)
-                    : launch_one<1, kBnOne, false, false, EPI_ROWS>(p, s);
+            return pair ? launch_one<2, 256, false, true, EPI_ROWS>(p, s)
+                        : launch_one<1, 128, false, true, EPI_ROWS>(p, s);
+        return pair ? launch_one<2, 256, false, false, EPI_ROWS>(p, s)
+                    : launch_one<1, 128, false, false, EPI_ROWS>(p, s);
     case EPI_NS:
         if (layout == A_K_B_MN)
-            return pair ? launch_one<2, kBnPair, false, true, EPI_NS>(p, s)
-                        : launch_one<1, kBnOne, false, true, EPI_NS>(p, s);
+            return pair ? launch_one<2, 256, false, true, EPI_NS>(p, s)
+                        : launch_one<1, 128, false, true, EPI_NS>(p, s);
         if (layout == A_MN_B_MN)
-            return pair ? launch_one<2, kBnPair, true, true, EPI_NS>(p, s)
-                        : launch_one<1, kBnOne, true, true, EPI_NS>(p, s);
-        return pair ? launch_one<2, kBnPair, false, false, EPI_NS>(p, s)
-                    : launch_one<1, kBnOne, false, false, EPI_NS>(p, s);
+            return pair ? launch_one<2, 256, true, true, EPI_NS>(p, s)
+                        : launch_one<1, 128, true, true, EPI_NS>(p, s);
+        return pair ? launch_one<2, 256, false, false, EPI_NS>(p, s)
+                    : launch_one<1, 128, false, false, EPI_NS>(p, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(256)
 
 struct Bufs {
     int32_t *status;
+    unsigned long long *counters;
+    float *partial;
     double *sums;
     float *scale;
     __half *X[2][2], *A, *B;   // X: [ping-pong][hi, lo]
@@ -211,6 +213,8 @@ Bufs carve(int64_t E, int64_t m, int64_t n, int steps, void *ws)
     const int64_t p = m < n ? m : n;
     const size_t x = (size_t)(E * m * up8(n)) * 2, a = (size_t)(E * p * up8(p)) * 2;
     b.status = static_cast<int32_t *>(take(256));
+    b.counters = static_cast<unsigned long long *>(take(kCounterBytes));
+    b.partial = static_cast<float *>(take(kPartialBytes));
     b.sums = static_cast<double *>(take((size_t)E * kMaxParts * 8));
     b.scale = static_cast<float *>(take((size_t)E * 4));
     for (int i = 0; i < 2; ++i)
@@ -270,8 +274,8 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     }
     if (err != cudaSuccess)
         return err;
-    const bool pair = p >= 256;
-    const int box = b_box_rows(EPI_NS, pair), mbox = mn_box_rows(EPI_NS, pair);
+    const Tiles tiles = p >= 256 ? PAIR_256 : ONE_128;
+    const int box = b_box_rows(EPI_NS, tiles), mbox = mn_box_rows(EPI_NS, tiles);
     int cur = 0;
     for (int i = 0; i < steps; ++i, cur ^= 1) {
         const bool last = i + 1 == steps;
@@ -281,6 +285,9 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         memset(&P, 0, sizeof P);
         P.nsets = 1;
         P.fp16 = 1;
+        P.counters = w.counters;
+        P.partial = w.partial;
+        P.partial_bytes = kPartialBytes;
         P.status = w.status;
         P.clear_status = i == 0;
         Set &t = P.set[0];
@@ -308,7 +315,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.scale_pow = 2;
         if (!ok)
             return cudaErrorInvalidValue;
-        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_K : A_MN_B_MN, pair, s)) != cudaSuccess)
+        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_K : A_MN_B_MN, tiles, s)) != cudaSuccess)
             return err;
 
         // B = b A + c A A
@@ -325,7 +332,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.scale = nullptr;
         if (!ok)
             return cudaErrorInvalidValue;
-        if ((err = launch_tc(P, EPI_NS, A_K_B_K, pair, s)) != cudaSuccess)
+        if ((err = launch_tc(P, EPI_NS, A_K_B_K, tiles, s)) != cudaSuccess)
             return err;
 
         // X = a X + B X (a X + X B)
@@ -355,7 +362,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.out_group = last ? mn : m * ldx;
         if (!ok)
             return cudaErrorInvalidValue;
-        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_MN : A_K_B_K, pair, s)) != cudaSuccess)
+        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_MN : A_K_B_K, tiles, s)) != cudaSuccess)
             return err;
     }
     return cudaSuccess;

@@ -25,6 +25,9 @@ using namespace grp;
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+// workspace of the grouped products in bf16: status word, counters and parts of
+// cut tiles
+constexpr size_t kGroupedBytes = kStatusBytes + kCounterBytes + kPartialBytes;
 constexpr int kMaxShared = 64;   // shared experts of one backward call (tile table)
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -38,30 +41,40 @@ struct Table {
     int n_rows;
 };
 
-Params tc_params(const Table &t, void *status, bool clear)
+Params tc_params(const Table &t, void *ws, bool clear)
 {
     Params p;
     memset(&p, 0, sizeof p);
     p.offsets = t.offsets;
     p.rows = t.rows;
     p.n_rows = t.n_rows;
-    p.status = static_cast<int32_t *>(status);
+    p.status = static_cast<int32_t *>(ws);
     p.clear_status = clear;
     return p;
 }
 
+// Lets a launch cut tiles, with the scratch behind the status word.
+void set_cut(Params &p, void *ws)
+{
+    char *base = static_cast<char *>(ws);
+    p.counters = reinterpret_cast<unsigned long long *>(base + kStatusBytes);
+    p.partial = reinterpret_cast<float *>(base + kStatusBytes + kCounterBytes);
+    p.partial_bytes = kPartialBytes;
+}
+
 // Products over short groups use 128-row tiles: a 256-row tile would mostly
 // compute rows of nobody.
-bool pair_rows(int64_t rows, int64_t groups) { return rows >= 384 * groups; }
+Tiles row_tiles(int64_t rows, int64_t groups) { return rows >= 384 * groups ? PAIR_256 : ONE_128; }
 // Weight gradients: 256 x 256 tiles once the matrix fills them.
-bool pair_dw(int64_t M, int64_t N) { return M >= 256 && N >= 256; }
+Tiles dw_tiles(int64_t M, int64_t N) { return M >= 256 && N >= 256 ? PAIR_256 : ONE_128; }
 
 // y [R, N] = x [R, K] W[g]^T, or with back: dx [R, K] = dy [R, N] W[g].
 cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *in, const void *W,
                     void *out, bool back, void *status, cudaStream_t s)
 {
     Params p = tc_params(t, status, true);
-    const bool pair = pair_rows(R, G);
+    // few rows a group: the weights' bytes are the work
+    const Tiles tiles = R <= 24ll * G ? ONE_32 : row_tiles(R, G);
     Set &a = p.set[0];
     p.nsets = 1;
     a.mode = RAGGED_M;
@@ -72,14 +85,19 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
     a.b_grouped = 1;
     a.ld = a.N;
     a.out = out;
-    bool ok = map_k(&a.a[0], in, R, a.K, a.K, 1, 0, 128);
+    bool ok = map_k(&a.a[0], in, R, a.K, a.K, 1, 0, tiles == ONE_32 ? 32 : 128);
     if (back)
-        ok &= map_mn(&a.b[0], W, N, K, K, G, (int64_t)N * K, mn_box_rows(EPI_ROWS, pair));
+        ok &= map_mn(&a.b[0], W, N, K, K, G, (int64_t)N * K, mn_box_rows(EPI_ROWS, tiles));
     else
-        ok &= map_k(&a.b[0], W, N, K, K, G, (int64_t)N * K, b_box_rows(EPI_ROWS, pair));
+        ok &= map_k(&a.b[0], W, N, K, K, G, (int64_t)N * K, b_box_rows(EPI_ROWS, tiles));
+    if (tiles == ONE_128) {
+        a.has_few = 1;
+        ok &= map_k(&a.a_few, in, R, a.K, a.K, 1, 0, 32);
+    }
     if (!ok)
         return cudaErrorInvalidValue;
-    return launch_tc(p, EPI_ROWS, back ? A_K_B_MN : A_K_B_K, pair, s);
+    set_cut(p, status);
+    return launch_tc(p, EPI_ROWS, back ? A_K_B_MN : A_K_B_K, tiles, s);
 }
 
 // One weight-gradient set: out[g] (M x N) (= add +) sum_r a[r, :]^T b[r, :].
@@ -174,6 +192,11 @@ moe_status check_grouped(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t
     return MOE_OK;
 }
 
+size_t grouped_bytes(int32_t dtype)
+{
+    return dtype == MOE_DTYPE_BF16 ? kGroupedBytes : kStatusBytes;
+}
+
 moe_status check_ws(const void *ws, size_t bytes, size_t need)
 {
     if (!ws)
@@ -195,7 +218,7 @@ moe_status rows_call(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K, 
     const uintptr_t al = dtype == MOE_DTYPE_BF16 ? 16 : 4;
     if (!aligned(in, al) || !aligned(W, al) || !aligned(out, al))
         return MOE_ERR_ALIGN;
-    if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK)
+    if ((st = check_ws(ws, ws_bytes, grouped_bytes(dtype))) != MOE_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Table t{offsets, rows, (int)R};
@@ -227,6 +250,8 @@ FfnScratch carve_ffn(const moe_config &c, void *ws)
         return p;
     };
     const size_t e = dtype_bytes(c.dtype);
+    if (c.dtype == MOE_DTYPE_BF16)
+        off = kGroupedBytes;
     const size_t r = (size_t)perm_rows(c) * c.d_ff * e;
     const size_t q = c.n_shared > 0 ? (size_t)c.n_shared * c.T * c.d_ff_shared * e : 0;
     const bool swiglu = c.act == MOE_ACT_SWIGLU;
@@ -251,14 +276,14 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     const int64_t R = t.n_rows;
     const int d = c.d, F = c.d_ff, E = c.E, S = c.n_shared, Fs = c.d_ff_shared, T = c.T;
     const bool swiglu = c.act == MOE_ACT_SWIGLU, shared = S > 0 && T > 0;
-    const bool pair = (int64_t)T * c.k >= 384ll * E;
+    const Tiles tiles = row_tiles((int64_t)T * c.k, E);
     const Epi epi = swiglu ? EPI_SWIGLU : EPI_GELU;
     cudaError_t e;
     bool ok = true;
 
     // h, du, dv from x and dy
     Params p = tc_params(t, status, true);
-    const int ubox = b_box_rows(epi, pair);
+    const int ubox = b_box_rows(epi, tiles);
     auto act_set = [&](Set &v, int mode, int groups, int64_t rows, int cols, const void *in,
                        const void *dout, const void *w1, const void *w3, const void *w2, void *h,
                        void *du, void *dv) {
@@ -267,6 +292,7 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         v.M = mode == DENSE ? (int)rows : 0;
         v.N = cols;
         v.K = d;
+        v.segs = v.period = 2;
         v.b_grouped = 1;
         v.ld = cols;
         v.out_group = rows * cols;
@@ -277,7 +303,7 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         ok &= map_k(&v.a[1], in, rows, d, d, 1, 0, 128);
         ok &= map_k(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d, ubox);
         ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d,
-                     mn_box_rows(epi, pair));
+                     mn_box_rows(epi, tiles));
         if (swiglu)
             ok &= map_k(&v.b3, w3, cols, d, d, groups, (int64_t)cols * d, ubox);
     };
@@ -289,7 +315,7 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     }
     if (!ok)
         return cudaErrorInvalidValue;
-    if ((e = launch_tc(p, epi, A_K_B_K, pair, s)) != cudaSuccess)
+    if ((e = launch_tc(p, epi, A_K_B_K, tiles, s)) != cudaSuccess)
         return e;
 
     // dx = du W1 (+ dv W3); shared: summed over the experts in the accumulator
@@ -311,11 +337,11 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         const int ag = mode == DENSE ? groups : 1;
         ok &= map_k(&v.a[0], du, rows, cols, cols, ag, rows * cols, 128);
         ok &= map_mn(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d,
-                     mn_box_rows(EPI_ROWS, pair));
+                     mn_box_rows(EPI_ROWS, tiles));
         if (swiglu) {
             ok &= map_k(&v.a[1], dv, rows, cols, cols, ag, rows * cols, 128);
             ok &= map_mn(&v.b[1], w3, cols, d, d, groups, (int64_t)cols * d,
-                         mn_box_rows(EPI_ROWS, pair));
+                         mn_box_rows(EPI_ROWS, tiles));
         }
     };
     dx_set(p.set[0], RAGGED_M, E, R, F, f.du, f.dv, a.W1, a.W3, a.dx);
@@ -326,14 +352,15 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     }
     if (!ok)
         return cudaErrorInvalidValue;
-    if ((e = launch_tc(p, EPI_ROWS, A_K_B_MN, pair, s)) != cudaSuccess)
+    set_cut(p, status);
+    if ((e = launch_tc(p, EPI_ROWS, A_K_B_MN, tiles, s)) != cudaSuccess)
         return e;
 
     // weight gradients
     p = tc_params(t, status, false);
     int n = 0;
-    const bool dw_pair = pair_dw(F, d);
-    const int box = mn_box_rows(EPI_DW, dw_pair);
+    const Tiles wt = dw_tiles(F, d);
+    const int box = mn_box_rows(EPI_DW, wt);
     auto add = [&](void *out) { return acc ? out : nullptr; };
     ok &= dw_set(p.set[n++], RAGGED_K, E, R, F, d, f.du, false, a.x_perm, false, add(a.dW1), a.dW1,
                  f32, box);
@@ -353,7 +380,8 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     p.nsets = n;
     if (!ok)
         return cudaErrorInvalidValue;
-    return launch_tc(p, EPI_DW, A_MN_B_MN, dw_pair, s);
+    set_cut(p, status);
+    return launch_tc(p, EPI_DW, A_MN_B_MN, wt, s);
 }
 
 // fp32: the same gradients one product at a time; h holds u until the
@@ -423,7 +451,7 @@ extern "C" {
 
 size_t moe_grouped_workspace_size(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K)
 {
-    return check_grouped(dtype, G, R, N, K) == MOE_OK ? kStatusBytes : 0;
+    return check_grouped(dtype, G, R, N, K) == MOE_OK ? grouped_bytes(dtype) : 0;
 }
 
 moe_status moe_grouped_matmul(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K,
@@ -458,7 +486,7 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
     const uintptr_t al = dtype == MOE_DTYPE_BF16 ? 16 : 4;
     if (!aligned(dy, al) || !aligned(x, al) || !aligned(dW, al) || !aligned(add, al))
         return MOE_ERR_ALIGN;
-    if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK)
+    if ((st = check_ws(ws, ws_bytes, grouped_bytes(dtype))) != MOE_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Table t{offsets, rows, (int)R};
@@ -470,12 +498,13 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
         return cuda_status(launch_simt(p, s));
     }
     Params p = tc_params(t, ws, true);
-    const bool pair = pair_dw(N, K);
+    const Tiles tiles = dw_tiles(N, K);
     p.nsets = 1;
     if (!dw_set(p.set[0], RAGGED_K, G, R, N, K, dy, false, x, false, add, dW,
-                dw_dtype == MOE_DTYPE_F32, mn_box_rows(EPI_DW, pair)))
+                dw_dtype == MOE_DTYPE_F32, mn_box_rows(EPI_DW, tiles)))
         return MOE_ERR_CUDA;
-    return cuda_status(launch_tc(p, EPI_DW, A_MN_B_MN, pair, s));
+    set_cut(p, ws);
+    return cuda_status(launch_tc(p, EPI_DW, A_MN_B_MN, tiles, s));
 }
 
 moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *Y_perm,

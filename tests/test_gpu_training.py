@@ -79,7 +79,8 @@ def test_grouped_products(sizes, aligned, N, K, dtype):
     mark = 7.0
     y = torch.full((R, N), mark, dtype=dtype, device="cuda")
     dx = torch.full((R, K), mark, dtype=dtype, device="cuda")
-    ws = moe.workspace(256, "cuda")
+    ws = moe.workspace(moe.lib().moe_grouped_workspace_size(int(dtype == BF), G, R, N, K), "cuda")
+    ws.fill_(255)   # whatever the workspace held must not show
     moe.moe_grouped_matmul(x, W, off, rows, y=y, ws=ws)
     assert moe.moe_device_status(ws) == 0
     moe.moe_grouped_matmul_dx(dy, W, off, rows, dx=dx, ws=ws)

@@ -13,7 +13,7 @@ ODD = ctypes.c_void_p(4096 + 2)
 F32, BF16 = 0, 1
 
 
-def rows_args(dtype=BF16, G=2, R=10, N=64, K=32, x=P, W=P, off=P, rows=None, y=P, ws=P, nb=256):
+def rows_args(dtype=BF16, G=2, R=10, N=64, K=32, x=P, W=P, off=P, rows=None, y=P, ws=P, nb=1 << 30):
     return dtype, G, R, N, K, x, W, off, rows, y, ws, nb, None
 
 
@@ -39,7 +39,7 @@ def test_grouped_products_check_their_arguments(call, kw, status):
     (dict(dW=ODD), _abi.MOE_ERR_ALIGN), (dict(nb=0), _abi.MOE_ERR_WORKSPACE)])
 def test_weight_gradient_checks_its_arguments(kw, status):
     a = dict(dtype=BF16, G=2, R=10, N=64, K=32, dy=P, x=P, off=P, rows=None, out=F32, add=None,
-             dW=P, ws=P, nb=256)
+             dW=P, ws=P, nb=1 << 30)
     a.update(kw)
     assert moe.lib().moe_grouped_matmul_dw(*a.values(), None) == status
 
