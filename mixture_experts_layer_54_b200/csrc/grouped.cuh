@@ -33,6 +33,7 @@ struct Set {
     int M, N, K;                 // output rows (not RAGGED_M), columns, contraction (not RAGGED_K)
     int segs, period, seg_grouped, has_few;
     int a_grouped, b_grouped;    // 1: the operand has one matrix per group
+    int a_wide, b_wide;          // 1: one box is a whole stage (all segments')
     int sym;                     // 1: out is symmetric; only tiles on or below the diagonal
     int ld;                      // row pitch of out (elements)
     int64_t out_group;           // elements between the groups' outputs (not RAGGED_M)
@@ -94,15 +95,20 @@ enum Tiles { PAIR_256, ONE_128, ONE_32 };
 
 cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s);
 
-// Maps of a [groups, rows, cols] 2-byte tensor with row pitch ld for the
-// operand's role (group_stride in elements).
+// Maps of a [groups, rows, cols] 2-byte tensor with row pitch ld (group_stride in
+// elements) for the operand's role: K-major (cols is the contraction), boxes of
+// box_rows; MN-major (rows is the contraction), boxes of box_cols.  wide: cols is
+// a multiple of 64 and one box is a whole stage (a_wide, b_wide of the Set).
 bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-           int64_t groups, int64_t group_stride, int box_rows);
+           int64_t groups, int64_t group_stride, int box_rows, int stage_k, bool wide);
 bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-            int64_t groups, int64_t group_stride, int box_rows);
-// Box rows of a K-major B, and of an MN-major operand, in launches of this shape.
-int b_box_rows(Epi epi, Tiles tiles);
-int mn_box_rows(Epi epi, Tiles tiles);
+            int64_t groups, int64_t group_stride, int stage_k, int box_cols, bool wide);
+inline bool is_wide(int64_t cols) { return cols % 64 == 0; }
+// Of launches of this shape: B's rows a box (A's: 128, or 32 on ONE_32), those of
+// W2 in the hidden gradients, and the contraction a stage holds.
+int b_box(Epi epi, Tiles tiles);
+int dh_box(Tiles tiles);
+int stage_k(Epi epi, Tiles tiles);
 
 }  // namespace grp
 }  // namespace moe

@@ -6,7 +6,10 @@
 // One persistent, warp-specialised kernel (TMA -> shared memory ->
 // tcgen05.mma -> TMEM -> registers -> global).  PAIR tiles take a 2-CTA
 // cluster: 256 output rows (128 a CTA) x BN columns, each CTA loading its rows
-// of A and half the rows of B.  Operands whose contraction index is the row
+// of A and half the rows of B.  A stage is 128 of K, one TMA instruction for each
+// operand where the contiguous extent is a multiple of 64 (the tensor is then
+// described as blocks of 64 columns and the box takes two), two otherwise: their
+// number bounds the loads.  Operands whose contraction index is the row
 // index of the stored matrix (W in dx, both in dW) are read as they lie: boxes
 // of 64 contiguous elements x a stage's contraction rows, and the MMA takes
 // them as MN-major, so nothing is transposed in memory.
@@ -267,14 +270,23 @@ __device__ __forceinline__ void commit_all(uint32_t bar)
         mma_commit(bar);
 }
 
-template <int CTAS>
+// PAIR: the barrier may be the other CTA's
+template <bool PAIR>
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0,
-                                         int c1, int c2)
+                                         int c1, int c2, int c3)
 {
-    if (CTAS == 2)
-        tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+            : "memory");
     else
-        tma_load_3d(dst, m, bar, c0, c1, c2);
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+            : "memory");
 }
 
 // Arrive on the leader's barrier with `bytes` to come by TMA.  Nothing this
@@ -632,11 +644,10 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                 // B rows of this CTA, and their first
                 const int b_rows = ACT ? (uv ? S::B_ROWS : BN / CTAS) : S::B_ROWS;
                 const int b_row = t.n0 + (uv && CTAS == 2 ? 0 : (int)rank * (BN / CTAS));
-                // a tile of few rows loads them in boxes of 32 (the MMA's other rows
-                // are whatever the stage holds; they are never stored)
-                const bool few = EPI == EPI_ROWS && s.has_few && t.mg - t.m0 <= 96;
-                const int a_box = few ? 32 : AR;
-                const int a_rows = few ? (t.mg - t.m0 + 31) / 32 * 32 : AR;
+                // a tile of few rows loads no more than 32 (the MMA's other rows are
+                // whatever the stage holds; they are never stored)
+                const bool few = EPI == EPI_ROWS && s.has_few && t.mg - t.m0 <= 32;
+                const int a_rows = few ? 32 : AR;
                 const CUtensorMap *am = few ? &s.a_few : &s.a[ph];
                 const CUtensorMap *bm = uv && rank == 1 ? &s.b3 : &s.b[bi];
                 const int end = min(t.kbs, t.b1 - sg * t.kbs);
@@ -648,10 +659,11 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                     }
                     const int rem = t.klen - kb * S::BK;
                     const int nks = rem >= S::BK ? KSUB : (rem + 63) / 64;
-                    // K-major: nks boxes of 64 of K; MN-major: one box of BK per 64 columns
+                    const bool a_wide = !few && s.a_wide, b_wide = s.b_wide;
+                    // K-major: nks pieces of 64 of K; MN-major: BK rows
                     const uint32_t bytes =
-                        (uint32_t)((A_MN ? KSUB : nks) * a_rows * 128 +
-                                   (b_mn ? KSUB : nks) * b_rows * 128);
+                        (uint32_t)((A_MN || a_wide ? KSUB : nks) * a_rows * 128 +
+                                   (b_mn || b_wide ? KSUB : nks) * b_rows * 128);
                     const uint32_t fb = CTAS == 2 ? map_to_rank(full_bar(stage), 0)
                                                   : full_bar(stage);
                     const uint32_t sa = sA + stage * KSUB * A_BYTES;
@@ -664,31 +676,35 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             mbar_expect_tx(tail_bar(stage), bytes);
                         else
                             arrive_bytes<CTAS>(fb, bytes);
-                        auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1,
-                                        int c2) {
+                        auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2,
+                                        int c3) {
                             if (EPI == EPI_DW && tail)
-                                tma_load_3d(dst, m, tail_bar(stage), c0, c1, c2);
+                                load_box<false>(dst, m, tail_bar(stage), c0, c1, c2, c3);
                             else
-                                load_box<CTAS>(dst, m, fb, c0, c1, c2);
+                                load_box<CTAS == 2>(dst, m, fb, c0, c1, c2, c3);
                         };
-                        if (A_MN) {
-                            load(sa, am, m_row, kc, ga);
-                            load(sa + S::MN_BLOCK, am, m_row + 64, kc, ga);
+                        if (a_wide) {
+                            load(sa, am, 0, A_MN ? kc : m_row, (A_MN ? m_row : kc) / 64, ga);
+                        } else if (A_MN) {
+                            load(sa, am, m_row, kc, 0, ga);
+                            load(sa + S::MN_BLOCK, am, m_row + 64, kc, 0, ga);
                         } else {
                             for (int ks = 0; ks < nks; ++ks)
-                                for (int r = 0; r < a_rows; r += a_box)
-                                    load(sa + ks * A_BYTES + r * 128, am, kc + ks * 64, m_row + r,
-                                         ga);
+                                load(sa + ks * A_BYTES, am, kc + ks * 64, m_row, 0, ga);
                         }
-                        if (b_mn) {
+                        if (b_wide) {
+                            load(sb, bm, 0, b_mn ? kc : b_row, (b_mn ? b_row : kc) / 64, gb);
+                            if (uv && CTAS == 1)
+                                load(sb + BN * 128, &s.b3, 0, b_row, kc / 64, gb);
+                        } else if (b_mn) {
                             for (int b = 0; b < b_rows / 64; ++b)
-                                load(sb + b * S::MN_BLOCK, bm, b_row + b * 64, kc, gb);
+                                load(sb + b * S::MN_BLOCK, bm, b_row + b * 64, kc, 0, gb);
                         } else {
                             for (int ks = 0; ks < nks; ++ks) {
-                                load(sb + ks * S::B_BYTES, bm, kc + ks * 64, b_row, gb);
+                                load(sb + ks * S::B_BYTES, bm, kc + ks * 64, b_row, 0, gb);
                                 if (uv && CTAS == 1)
                                     load(sb + ks * S::B_BYTES + BN * 128, &s.b3, kc + ks * 64,
-                                         b_row, gb);
+                                         b_row, 0, gb);
                             }
                         }
                     }
@@ -1237,26 +1253,53 @@ constexpr int kBnAct = 128;
 
 }  // namespace
 
-bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-           int64_t groups, int64_t group_stride, int box_rows)
+namespace {
+
+// [groups, rows, cols] 2-byte elements, row pitch ld, as (64, rows, cols / 64,
+// groups) with boxes of `blocks` blocks of 64 columns (wide), or as (cols, rows,
+// 1, groups) with boxes of 64 columns.
+bool map_4d(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
+            int64_t groups, int64_t group_stride, int box_rows, int blocks)
 {
-    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 64, box_rows,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
+    EncodeTiled enc = encoder();
+    if (!enc)
+        return false;
+    const bool wide = blocks > 0;
+    const cuuint64_t far = (cuuint64_t)(group_stride > 0 ? group_stride : rows * ld) * 2;
+    cuuint64_t dims[4] = {(cuuint64_t)(wide ? 64 : cols), (cuuint64_t)rows,
+                          (cuuint64_t)(wide ? cols / 64 : 1), (cuuint64_t)groups};
+    cuuint64_t strides[3] = {(cuuint64_t)ld * 2, wide ? 128 : far, far};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)(wide ? blocks : 1), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool map_k(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
+           int64_t groups, int64_t group_stride, int box_rows, int stage_k, bool wide)
+{
+    return map_4d(m, base, rows, cols, ld, groups, group_stride, box_rows,
+                  wide ? stage_k / 64 : 0);
 }
 
 bool map_mn(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-            int64_t groups, int64_t group_stride, int box_rows)
+            int64_t groups, int64_t group_stride, int stage_k, int box_cols, bool wide)
 {
-    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 64, box_rows,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
+    return map_4d(m, base, rows, cols, ld, groups, group_stride, stage_k, wide ? box_cols / 64 : 0);
 }
 
-int b_box_rows(Epi epi, Tiles tiles)   // SwiGLU: a box of W1 and one of W3
+int b_box(Epi epi, Tiles tiles)   // SwiGLU: a box of W1 and one of W3
 {
     return epi == EPI_GELU && tiles == PAIR_256 ? kBnAct / 2 : 128;
 }
 
-int mn_box_rows(Epi epi, Tiles tiles) { return epi == EPI_SWIGLU && tiles != PAIR_256 ? 64 : 128; }
+int dh_box(Tiles tiles) { return tiles == PAIR_256 ? kBnAct / 2 : kBnAct; }
+
+int stage_k(Epi epi, Tiles tiles) { return epi == EPI_SWIGLU && tiles != PAIR_256 ? 64 : 128; }
 
 cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s)
 {

@@ -275,7 +275,8 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     if (err != cudaSuccess)
         return err;
     const Tiles tiles = p >= 256 ? PAIR_256 : ONE_128;
-    const int box = b_box_rows(EPI_NS, tiles), mbox = mn_box_rows(EPI_NS, tiles);
+    const int box = b_box(EPI_NS, tiles), sk = stage_k(EPI_NS, tiles);
+    const bool nw = is_wide(n), pw = is_wide(p);
     int cur = 0;
     for (int i = 0; i < steps; ++i, cur ^= 1) {
         const bool last = i + 1 == steps;
@@ -300,12 +301,13 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.M = t.N = p;
         t.K = q;
         t.sym = 1;
+        t.a_wide = t.b_wide = nw;
         if (wide) {
-            ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128);
-            ok &= map_k(&t.b[0], X, m, n, ldx, E, m * ldx, box);
+            ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128, sk, nw);
+            ok &= map_k(&t.b[0], X, m, n, ldx, E, m * ldx, box, sk, nw);
         } else {
-            ok &= map_mn(&t.a[0], X, m, n, ldx, E, m * ldx, mbox);
-            t.b[0] = t.a[0];
+            ok &= map_mn(&t.a[0], X, m, n, ldx, E, m * ldx, sk, 128, nw);
+            ok &= map_mn(&t.b[0], X, m, n, ldx, E, m * ldx, sk, box, nw);
         }
         t.out = w.A;
         t.ld = (int)lda;
@@ -321,8 +323,9 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         // B = b A + c A A
         P.clear_status = 0;
         t.K = p;
-        ok &= map_k(&t.a[0], w.A, p, p, lda, E, p * lda, 128);
-        ok &= map_k(&t.b[0], w.A, p, p, lda, E, p * lda, box);
+        t.a_wide = t.b_wide = pw;
+        ok &= map_k(&t.a[0], w.A, p, p, lda, E, p * lda, 128, sk, pw);
+        ok &= map_k(&t.b[0], w.A, p, p, lda, E, p * lda, box, sk, pw);
         t.out = w.B;
         t.alpha = c * kSB / (kSA * kSA);
         t.beta = b * kSB / kSA;
@@ -339,12 +342,14 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.sym = 0;
         t.M = m;
         t.N = n;
+        t.a_wide = wide ? pw : nw;
+        t.b_wide = wide ? nw : pw;
         if (wide) {
-            ok &= map_k(&t.a[0], w.B, p, p, lda, E, p * lda, 128);
-            ok &= map_mn(&t.b[0], X, m, n, ldx, E, m * ldx, mbox);
+            ok &= map_k(&t.a[0], w.B, p, p, lda, E, p * lda, 128, sk, pw);
+            ok &= map_mn(&t.b[0], X, m, n, ldx, E, m * ldx, sk, box, nw);
         } else {
-            ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128);
-            ok &= map_k(&t.b[0], w.B, p, p, lda, E, p * lda, box);
+            ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128, sk, nw);
+            ok &= map_k(&t.b[0], w.B, p, p, lda, E, p * lda, box, sk, pw);
         }
         const float mult = last ? scale : kSX;
         t.alpha = i == 0 ? mult / kSB : mult / (kSB * kSX);

@@ -85,14 +85,17 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
     a.b_grouped = 1;
     a.ld = a.N;
     a.out = out;
-    bool ok = map_k(&a.a[0], in, R, a.K, a.K, 1, 0, tiles == ONE_32 ? 32 : 128);
+    const int sk = stage_k(EPI_ROWS, tiles), box = b_box(EPI_ROWS, tiles);
+    a.a_wide = is_wide(a.K);
+    a.b_wide = is_wide(K);
+    bool ok = map_k(&a.a[0], in, R, a.K, a.K, 1, 0, tiles == ONE_32 ? 32 : 128, sk, a.a_wide);
     if (back)
-        ok &= map_mn(&a.b[0], W, N, K, K, G, (int64_t)N * K, mn_box_rows(EPI_ROWS, tiles));
+        ok &= map_mn(&a.b[0], W, N, K, K, G, (int64_t)N * K, sk, box, a.b_wide);
     else
-        ok &= map_k(&a.b[0], W, N, K, K, G, (int64_t)N * K, b_box_rows(EPI_ROWS, tiles));
+        ok &= map_k(&a.b[0], W, N, K, K, G, (int64_t)N * K, box, sk, a.b_wide);
     if (tiles == ONE_128) {
         a.has_few = 1;
-        ok &= map_k(&a.a_few, in, R, a.K, a.K, 1, 0, 32);
+        ok &= map_k(&a.a_few, in, R, a.K, a.K, 1, 0, 32, sk, false);
     }
     if (!ok)
         return cudaErrorInvalidValue;
@@ -102,7 +105,7 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
 
 // One weight-gradient set: out[g] (M x N) (= add +) sum_r a[r, :]^T b[r, :].
 bool dw_set(Set &t, int mode, int groups, int64_t rows, int M, int N, const void *a, bool a_grouped,
-            const void *b, bool b_grouped, const void *add, void *out, bool f32, int box)
+            const void *b, bool b_grouped, const void *add, void *out, bool f32, Tiles tiles)
 {
     t.mode = mode;
     t.groups = groups;
@@ -120,8 +123,12 @@ bool dw_set(Set &t, int mode, int groups, int64_t rows, int M, int N, const void
     // no rows: nothing is loaded, the maps only have to be valid
     const int64_t r = rows > 0 ? rows : 1;
     const void *pa = rows > 0 ? a : out, *pb = rows > 0 ? b : out;
-    return map_mn(&t.a[0], pa, r, M, M, a_grouped ? groups : 1, r * M, box) &&
-           map_mn(&t.b[0], pb, r, N, N, b_grouped ? groups : 1, r * N, box);
+    const int sk = stage_k(EPI_DW, tiles);
+    t.a_wide = is_wide(M);
+    t.b_wide = is_wide(N);
+    return map_mn(&t.a[0], pa, r, M, M, a_grouped ? groups : 1, r * M, sk, 128, t.a_wide) &&
+           map_mn(&t.b[0], pb, r, N, N, b_grouped ? groups : 1, r * N, sk, b_box(EPI_DW, tiles),
+                  t.b_wide);
 }
 
 Simt simt_rows(const Table &t, int mode, int G, int M, int N, int K, const float *in,
@@ -283,7 +290,7 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
 
     // h, du, dv from x and dy
     Params p = tc_params(t, status, true);
-    const int ubox = b_box_rows(epi, tiles);
+    const int ubox = b_box(epi, tiles), ask = stage_k(epi, tiles);   // widths: multiples of 64
     auto act_set = [&](Set &v, int mode, int groups, int64_t rows, int cols, const void *in,
                        const void *dout, const void *w1, const void *w3, const void *w2, void *h,
                        void *du, void *dv) {
@@ -299,13 +306,14 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         v.out = h;
         v.out2 = du;
         v.out3 = dv;
-        ok &= map_k(&v.a[0], dout, rows, d, d, 1, 0, 128);
-        ok &= map_k(&v.a[1], in, rows, d, d, 1, 0, 128);
-        ok &= map_k(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d, ubox);
-        ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d,
-                     mn_box_rows(epi, tiles));
+        v.a_wide = v.b_wide = 1;
+        ok &= map_k(&v.a[0], dout, rows, d, d, 1, 0, 128, ask, true);
+        ok &= map_k(&v.a[1], in, rows, d, d, 1, 0, 128, ask, true);
+        ok &= map_k(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d, ubox, ask, true);
+        ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d, ask, dh_box(tiles),
+                     true);
         if (swiglu)
-            ok &= map_k(&v.b3, w3, cols, d, d, groups, (int64_t)cols * d, ubox);
+            ok &= map_k(&v.b3, w3, cols, d, d, groups, (int64_t)cols * d, ubox, ask, true);
     };
     act_set(p.set[0], RAGGED_M, E, R, F, a.x_perm, a.dY, a.W1, a.W3, a.W2, f.h, f.du, f.dv);
     p.nsets = 1;
@@ -334,14 +342,14 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         v.b_grouped = 1;
         v.ld = d;
         v.out = out;
-        const int ag = mode == DENSE ? groups : 1;
-        ok &= map_k(&v.a[0], du, rows, cols, cols, ag, rows * cols, 128);
-        ok &= map_mn(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d,
-                     mn_box_rows(EPI_ROWS, tiles));
+        const int ag = mode == DENSE ? groups : 1, sk = stage_k(EPI_ROWS, tiles);
+        const int box = b_box(EPI_ROWS, tiles);
+        v.a_wide = v.b_wide = 1;
+        ok &= map_k(&v.a[0], du, rows, cols, cols, ag, rows * cols, 128, sk, true);
+        ok &= map_mn(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d, sk, box, true);
         if (swiglu) {
-            ok &= map_k(&v.a[1], dv, rows, cols, cols, ag, rows * cols, 128);
-            ok &= map_mn(&v.b[1], w3, cols, d, d, groups, (int64_t)cols * d,
-                         mn_box_rows(EPI_ROWS, tiles));
+            ok &= map_k(&v.a[1], dv, rows, cols, cols, ag, rows * cols, 128, sk, true);
+            ok &= map_mn(&v.b[1], w3, cols, d, d, groups, (int64_t)cols * d, sk, box, true);
         }
     };
     dx_set(p.set[0], RAGGED_M, E, R, F, f.du, f.dv, a.W1, a.W3, a.dx);
@@ -360,22 +368,21 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     p = tc_params(t, status, false);
     int n = 0;
     const Tiles wt = dw_tiles(F, d);
-    const int box = mn_box_rows(EPI_DW, wt);
     auto add = [&](void *out) { return acc ? out : nullptr; };
     ok &= dw_set(p.set[n++], RAGGED_K, E, R, F, d, f.du, false, a.x_perm, false, add(a.dW1), a.dW1,
-                 f32, box);
+                 f32, wt);
     if (swiglu)
         ok &= dw_set(p.set[n++], RAGGED_K, E, R, F, d, f.dv, false, a.x_perm, false, add(a.dW3),
-                     a.dW3, f32, box);
-    ok &= dw_set(p.set[n++], RAGGED_K, E, R, d, F, a.dY, false, f.h, false, add(a.dW2), a.dW2, f32, box);
+                     a.dW3, f32, wt);
+    ok &= dw_set(p.set[n++], RAGGED_K, E, R, d, F, a.dY, false, f.h, false, add(a.dW2), a.dW2, f32, wt);
     if (S > 0) {
         ok &= dw_set(p.set[n++], DENSE, S, T, Fs, d, f.dus, true, a.x, false, add(a.dWs1), a.dWs1,
-                     f32, box);
+                     f32, wt);
         if (swiglu)
             ok &= dw_set(p.set[n++], DENSE, S, T, Fs, d, f.dvs, true, a.x, false, add(a.dWs3),
-                         a.dWs3, f32, box);
+                         a.dWs3, f32, wt);
         ok &= dw_set(p.set[n++], DENSE, S, T, d, Fs, a.dy, false, f.hs, true, add(a.dWs2), a.dWs2,
-                     f32, box);
+                     f32, wt);
     }
     p.nsets = n;
     if (!ok)
@@ -501,7 +508,7 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
     const Tiles tiles = dw_tiles(N, K);
     p.nsets = 1;
     if (!dw_set(p.set[0], RAGGED_K, G, R, N, K, dy, false, x, false, add, dW,
-                dw_dtype == MOE_DTYPE_F32, mn_box_rows(EPI_DW, tiles)))
+                dw_dtype == MOE_DTYPE_F32, tiles))
         return MOE_ERR_CUDA;
     set_cut(p, ws);
     return cuda_status(launch_tc(p, EPI_DW, A_MN_B_MN, tiles, s));
