@@ -41,9 +41,10 @@ struct Set {
     void *out2, *out3;           // EPI_GELU / EPI_SWIGLU: du, dv; EPI_NS: out2
     const void *add;             // EPI_DW, nullable: added before the rounding
     int out_f32;                 // EPI_DW
-    // EPI_NS: val = alpha acc + beta base, stored as fp16 (out2: what the
-    // rounding lost, as another fp16) or as bf16
-    const void *base, *base2;    // nullable; base2: base's own second term
+    // EPI_NS: val = alpha acc + beta base (+ diag on the diagonal), stored as fp16
+    // (out2: what the rounding lost, as another fp16) or as bf16
+    const void *base;            // nullable
+    float diag;
     int base_ld, out_bf16;
     int64_t base_group;
     float alpha, beta;

@@ -458,17 +458,6 @@ __device__ __forceinline__ float2 unpack_fp16(uint32_t u)
     return __half22float2(*reinterpret_cast<__half2 *>(&u));
 }
 
-// Both terms of base, 32 columns of this lane's row from element `at` on.
-__device__ __forceinline__ void load_base(const Set &s, int64_t at, int cv, uint32_t *hi,
-                                          uint32_t *lo)
-{
-    load_row<2>(reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base) + at), 2 * cv,
-                s.base_bytes, hi);
-    if (s.base2)
-        load_row<2>(reinterpret_cast<const uint8_t *>(static_cast<const __half *>(s.base2) + at),
-                    2 * cv, s.base_bytes, lo);
-}
-
 // The mirrored place of 32 columns (w: pairs of columns of this lane's row):
 // out points at column 0's place for row 0 of the warp.  Two exchanges give a
 // lane one column's values for four rows, so a warp stores 64-byte pieces, 8
@@ -559,12 +548,13 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     pdl_trigger();
     if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0)
         *p.status = 0;
+    if (p.set[0].mode != DENSE) {   // the segment table, all groups' reads in flight at once
+        for (int g = threadIdx.x; g < p.set[0].groups; g += S::THREADS)
+            group_rows(p.offsets, p.rows, p.n_rows, g, &span[g].x, &span[g].y);
+        __syncthreads();
+    }
     if (warp == 2) {
-        // the segment table, and the tile table: running sum of the entries' tiles
-        if (p.set[0].mode != DENSE)
-            for (int g = lane; g < p.set[0].groups; g += 32)
-                group_rows(p.offsets, p.rows, p.n_rows, g, &span[g].x, &span[g].y);
-        __syncwarp();
+        // the tile table: running sum of the entries' tiles
         int base = 0;
         for (int e0 = 0; e0 < p.entries; e0 += 32) {
             const int e = e0 + lane;
@@ -894,14 +884,15 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
             const int rv = AR < 128 && q > 0 ? 0 : t.mg - m;
             const int c_end = rv > 0 ? min((half + 1) * (BN / 2), s.N - t.n0) : 0;
             // base is read a chunk ahead: the first before the products are done
-            uint32_t bhi[EPI == EPI_NS ? 16 : 1], blo[EPI == EPI_NS ? 16 : 1];
+            uint32_t base[EPI == EPI_NS ? 16 : 1];
             const bool based = EPI == EPI_NS && s.base && lane < rv;
-            const int64_t base0 =
-                (int64_t)t.g * s.base_group + (int64_t)(m + lane) * s.base_ld + t.n0;
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(
+                static_cast<const __half *>(s.base) + (int64_t)t.g * s.base_group +
+                (int64_t)(m + lane) * s.base_ld + t.n0);
             if constexpr (EPI == EPI_NS) {
                 const int c = half * (BN / 2);
                 if (based && c < c_end)
-                    load_base(s, base0 + c, s.N - t.n0 - c, bhi, blo);
+                    load_row<2>(from + 2 * c, 2 * (s.N - t.n0 - c), s.base_bytes, base);
             }
             if (!wait_bar(tfull_bar(slot), (it >> 1) & 1, ctl))
                 break;
@@ -1142,16 +1133,17 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                         if (based) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                float2 f = unpack_fp16(bhi[i]);
-                                if (s.base2) {
-                                    const float2 l = unpack_fp16(blo[i]);
-                                    f.x += l.x, f.y += l.y;
-                                }
+                                const float2 f = unpack_fp16(base[i]);
                                 v[2 * i] += beta * f.x;
                                 v[2 * i + 1] += beta * f.y;
                             }
                             if (c + 32 < c_end)
-                                load_base(s, base0 + c + 32, cv - 32, bhi, blo);
+                                load_row<2>(from + 2 * (c + 32), 2 * (cv - 32), s.base_bytes, base);
+                        }
+                        if (s.diag != 0.f && t.n0 + c < m + 32 && m < t.n0 + c + 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] += t.n0 + c + i == m + lane ? s.diag : 0.f;
                         }
                         uint16_t *hi = static_cast<uint16_t *>(s.out) + at;
                         if (s.out_bf16) {
@@ -1316,8 +1308,7 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream
                              reinterpret_cast<uint64_t>(v.add);
         v.bytes = all % 32 == 0 ? 32 : (all % 16 == 0 ? 16 : 2);
         const uint64_t base = (uint64_t)(v.base_ld * 2) | (uint64_t)(v.base_group * 2) |
-                              reinterpret_cast<uint64_t>(v.base) |
-                              reinterpret_cast<uint64_t>(v.base2);
+                              reinterpret_cast<uint64_t>(v.base);
         v.base_bytes = base % 32 == 0 ? 32 : 16;
         ents += p.set[i].groups;
     }

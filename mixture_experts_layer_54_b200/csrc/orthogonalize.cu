@@ -12,12 +12,14 @@
 // update of rank 32, measured.  That noise only passes through a X, since B
 // multiplies those directions by almost nothing; so X is held as two fp16
 // terms (hi + lo, 22 bits), a X takes both and the products only hi.  The
-// result is then within 2e-3 of the 64-bit one (2-norm; 1.6e-3 for noise, 1e-3
-// and less for decaying spectra), at the cost of one product each, where two
-// terms in every product cost 2.6 times as much for 8e-4.  The last step reads
-// hi alone: near singular value 1 the same X in both places is the more exact.
-// A bf16 G times a power of two is exact in one term.  A and B are symmetric:
-// only tiles on or below the diagonal are computed and mirrored.
+// result is then within 2e-3 of the 64-bit one (2-norm; 1.4e-3 for noise, 6e-4
+// for decaying spectra, 1.8e-3 for rank 32), at the cost of one product each,
+// where two terms in every product cost 2.6 times as much for 8e-4.  a hi comes
+// with the product, as a on B's diagonal (one array less to read in its
+// epilogue: 8 to 6 bytes an element), and the last step reads hi alone: near
+// singular value 1 the same X in both places is the more exact.  A bf16 G times
+// a power of two is exact in one term.  A and B are symmetric: only tiles on or
+// below the diagonal are computed and mirrored.
 #include "grouped.cuh"
 
 #include <cuda_fp16.h>
@@ -320,7 +322,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_K : A_MN_B_MN, tiles, s)) != cudaSuccess)
             return err;
 
-        // B = b A + c A A
+        // B = a I + b A + c A A
         P.clear_status = 0;
         t.K = p;
         t.a_wide = t.b_wide = pw;
@@ -329,6 +331,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.out = w.B;
         t.alpha = c * kSB / (kSA * kSA);
         t.beta = b * kSB / kSA;
+        t.diag = a * kSB;
         t.base = w.A;
         t.base_ld = (int)lda;
         t.base_group = p * lda;
@@ -338,8 +341,9 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         if ((err = launch_tc(P, EPI_NS, A_K_B_K, tiles, s)) != cudaSuccess)
             return err;
 
-        // X = a X + B X (a X + X B)
+        // X = B hi + a lo (hi B + a lo)
         t.sym = 0;
+        t.diag = 0.f;
         t.M = m;
         t.N = n;
         t.a_wide = wide ? pw : nw;
@@ -356,8 +360,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.beta = i == 0 ? a * mult : a * mult / kSX;
         t.scale = i == 0 ? w.scale : nullptr;
         t.scale_pow = 1;
-        t.base = X;
-        t.base2 = Xlo;
+        t.base = Xlo;
         t.base_ld = (int)ldx;
         t.base_group = m * ldx;
         t.out = last ? U : w.X[cur ^ 1][0];
