@@ -53,7 +53,8 @@ def test_workspace_sizes():
     R = moe.moe_perm_rows(cfg)
     assert moe.moe_ffn_backward_workspace_size(cfg) >= 3 * 2 * (R * 192 + 2 * 100 * 64)
     assert moe.moe_ffn_backward_workspace_size(moe.moe_config(cfg, d_ff=100)) == 0
-    assert moe.moe_orthogonalize_workspace_size(3, 100, 50) >= 3 * (8 * 100 * 50 + 4 * 50 * 50)
+    assert moe.moe_orthogonalize_workspace_size(3, 100, 50) >= 256
+    assert moe.moe_orthogonalize_workspace_size(3, 500, 200) >= 3 * (8 * 500 * 200 + 4 * 200 * 200)
     for bad in ((0, 8, 8, 5), (1025, 8, 8, 5), (1, 0, 8, 5), (1, 8, 0, 5), (1, 8, 8, 0),
                 (1, 8, 8, 33), (1, (1 << 20) + 1, 8, 5)):
         assert moe.moe_orthogonalize_workspace_size(*bad) == 0
@@ -67,7 +68,7 @@ def test_workspace_sizes():
     (dict(coeffs=(float("nan"), 0, 0)), _abi.MOE_ERR_SHAPE),
     (dict(U=ctypes.c_void_p(4097)), _abi.MOE_ERR_ALIGN), (dict(nb=256), _abi.MOE_ERR_WORKSPACE)])
 def test_orthogonalize_checks_its_arguments(kw, status):
-    a = dict(dtype=BF16, E=2, m=16, n=24, G=P, steps=5, coeffs=(3.0, -4.0, 2.0), eps=1e-7,
+    a = dict(dtype=BF16, E=2, m=160, n=240, G=P, steps=5, coeffs=(3.0, -4.0, 2.0), eps=1e-7,
              scale=1.0, U=P, ws=P, nb=1 << 30)
     a.update(kw)
     a["coeffs"] = (ctypes.c_float * 3)(*a["coeffs"])
