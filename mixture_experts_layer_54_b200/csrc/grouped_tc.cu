@@ -348,8 +348,8 @@ __device__ __forceinline__ void st16(void *p, const uint32_t *w)
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 32 columns of packed 16-bit values of this lane's row, the first cv of them
-// (a multiple of 8 unless bytes is 2) to dst.  bytes: what every row is aligned to.
+// 32 columns of packed 16-bit values of this lane's row, the first cv of them (a
+// multiple of 8) to dst.  bytes: what every row is aligned to.
 __device__ __forceinline__ void store16(const uint32_t *w, uint16_t *dst, int cv, int bytes)
 {
     if (bytes == 32) {
@@ -357,16 +357,11 @@ __device__ __forceinline__ void store16(const uint32_t *w, uint16_t *dst, int cv
         for (int c = 0; c < 2; ++c)
             if (16 * c < cv)
                 st32(dst + 16 * c, w + 8 * c);
-    } else if (bytes == 16) {
+    } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             if (8 * c < cv)
                 st16(dst + 8 * c, w + 4 * c);
-    } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-            if (c < cv)
-                dst[c] = (uint16_t)(w[c / 2] >> (16 * (c & 1)));
     }
 }
 
@@ -437,6 +432,24 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, uint8_t *stg, 
                      : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
+}
+
+// The same tile to rows of any alignment: a warp writes one row's 32 values at a
+// time.  out: column 0 of row 0; rv rows and cv columns are stored.
+__device__ __forceinline__ void store_odd(uint8_t *stg, int lane, const uint32_t *w, uint16_t *out,
+                                          int64_t ld, int rv, int cv)
+{
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+    __syncwarp();
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+        if (r < rv && lane < cv)
+            out[r * ld + lane] = *reinterpret_cast<const uint16_t *>(
+                stg + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
 }
 
 // This warp's part of a cut tile is written; true for the last of the parts,
@@ -1195,8 +1208,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                                 w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
                             if (s.c_map)
                                 store_box(&s.c[0], stg, lane, w, t.n0 + c, m, t.g);
-                            else if (mine)
-                                store16(w, hi, cv, bytes);
+                            else
+                                store_odd(stg, lane, w, hi - (int64_t)lane * s.ld, s.ld, rv, cv);
                             continue;
                         }
 #pragma unroll

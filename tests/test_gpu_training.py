@@ -330,7 +330,8 @@ NS_TOL = 2.0 ** -8 + 16 * 2.0 ** -11
 
 @pytest.mark.parametrize("E,m,n", [(1, 1, 1), (2, 1, 40), (3, 37, 51), (2, 51, 37), (4, 64, 32),
                                    (2, 300, 700), (3, 520, 264), (1, 256, 1000), (1, 130, 4100),
-                                   (2, 129, 129), (5, 16, 16)])
+                                   (2, 129, 129), (5, 16, 16),
+                                   (1, 128, 320), (2, 320, 128), (1, 128, 321), (200, 24, 72)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("kind", ["noise", "low_rank"])
 def test_orthogonalize(E, m, n, dtype, kind):
