@@ -945,6 +945,17 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
             const uint8_t *from = reinterpret_cast<const uint8_t *>(
                 static_cast<const __half *>(s.base) + (int64_t)t.g * s.base_group +
                 (int64_t)(m + lane) * s.base_ld + t.n0);
+            if constexpr (EPI == EPI_DW) {
+                // the addend's lines on their way to L2 while the products run
+                if (s.add && lane < rv) {
+                    const int esz = s.out_f32 ? 4 : 2, c = half * (BN / 2);
+                    const uint8_t *row = static_cast<const uint8_t *>(s.add) +
+                                         ((int64_t)t.g * s.out_group +
+                                          (int64_t)(m + lane) * s.ld + t.n0 + c) * esz;
+                    for (int b = 0; b < (c_end - c) * esz; b += 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + b));
+                }
+            }
             if constexpr (EPI == EPI_NS) {
                 const int c = half * (BN / 2);
                 if (based && c < c_end)

@@ -192,6 +192,21 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Tiles of E products of M x N over K: a round of 256 x 256 tiles on SM pairs
+// costs its contraction (0.8 us for 128, bound by the loads, and as much for 128
+// x 128 tiles on single SMs) and 8 us at its end, where the small tiles take 4;
+// four times as many of them go two to a pair.
+Tiles ns_tiles(int E, int M, int N, int K, bool sym)
+{
+    auto rounds = [&](int t, int units) {
+        const int64_t r = ceil_div(M, t), c = ceil_div(N, t);
+        return ceil_div(E * (sym ? r * (r + 1) / 2 : r * c), units);
+    };
+    const int sms = device_sms();
+    const double k = 0.8 * ceil_div(K, 128);
+    return rounds(256, sms / 2) * (k + 8) <= rounds(128, sms) * (k + 4) ? PAIR_256 : ONE_128;
+}
+
 struct Bufs {
     int32_t *status;
     unsigned long long *counters;
@@ -286,8 +301,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     }
     if (err != cudaSuccess)
         return err;
-    const Tiles tiles = p >= 256 ? PAIR_256 : ONE_128;
-    const int box = b_box(EPI_NS, tiles), sk = stage_k(EPI_NS, tiles);
+    const int box = b_box(EPI_NS, PAIR_256), sk = stage_k(EPI_NS, PAIR_256);   // the same for ONE_128
     const bool nw = is_wide(n), pw = is_wide(p);
     int cur = 0;
     for (int i = 0; i < steps; ++i, cur ^= 1) {
@@ -329,7 +343,8 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.scale_pow = 2;
         if (!ok)
             return cudaErrorInvalidValue;
-        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_K : A_MN_B_MN, tiles, s)) != cudaSuccess)
+        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_K : A_MN_B_MN,
+                             ns_tiles(E, p, p, q, true), s)) != cudaSuccess)
             return err;
 
         // B = a I + b A + c A A
@@ -348,7 +363,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.scale = nullptr;
         if (!ok)
             return cudaErrorInvalidValue;
-        if ((err = launch_tc(P, EPI_NS, A_K_B_K, tiles, s)) != cudaSuccess)
+        if ((err = launch_tc(P, EPI_NS, A_K_B_K, ns_tiles(E, p, p, p, true), s)) != cudaSuccess)
             return err;
 
         // X = B hi + a lo (hi B + a lo)
@@ -380,7 +395,8 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.out_group = last ? mn : m * ldx;
         if (!ok)
             return cudaErrorInvalidValue;
-        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_MN : A_K_B_K, tiles, s)) != cudaSuccess)
+        if ((err = launch_tc(P, EPI_NS, wide ? A_K_B_MN : A_K_B_K,
+                             ns_tiles(E, m, n, p, false), s)) != cudaSuccess)
             return err;
     }
     return cudaSuccess;
