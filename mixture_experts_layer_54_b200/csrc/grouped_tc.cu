@@ -334,6 +334,12 @@ __device__ __forceinline__ void arrive_written(uint32_t bar)
         mbar_arrive(bar);
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
 // Every lane stores its own row, 32 bytes at a time where the rows start on
 // 32-byte boundaries (whole sectors; a warp's 32 rows through a staging tile in
 // shared memory to 64-byte pieces measured 3 times as long), else 16.
@@ -394,6 +400,7 @@ __device__ __forceinline__ void load_row(const uint8_t *p, int end, int bytes, u
         }
     }
 }
+// n 32-byte pieces of a row, those that begin before byte `end`
 template <int N>
 __device__ __forceinline__ void store_row(uint8_t *p, int end, int bytes, const uint32_t *w)
 {
@@ -407,6 +414,136 @@ __device__ __forceinline__ void store_row(uint8_t *p, int end, int bytes, const 
             for (int h = 0; h < 2; ++h)
                 if (32 * c + 16 * h < end)
                     st16(p + 32 * c + 16 * h, w + 8 * c + 4 * h);
+        }
+    }
+}
+
+// 4 x 4 transpose of 32-byte blocks over four neighbouring lanes: lane q of them
+// holds row q's blocks 0..3 before, block q of rows 0..3 after.
+__device__ __forceinline__ void transpose_blocks(uint32_t (&w)[4][8], int lane)
+{
+    const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {   // blocks k, k + 1 with the odd/even neighbour
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, b0 ? w[k][j] : w[k + 1][j], 1);
+            if (b0)
+                w[k][j] = o;
+            else
+                w[k + 1][j] = o;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {      // blocks k, k + 2 with the neighbour two lanes on
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, b1 ? w[k][j] : w[k + 2][j], 2);
+            if (b1)
+                w[k][j] = o;
+            else
+                w[k + 2][j] = o;
+        }
+    }
+}
+
+// This lane's row of N sums (plus the addend) to fp32 or bf16.  at: element
+// (row 0 of the warp, first column); rv rows and cols columns are stored.
+// Without an addend four lanes trade blocks first, so that a row's 128 bytes
+// leave in one instruction: lanes storing 32 bytes of a row each cost the load
+// and store unit 32 lines an instruction (393 to 333 us for two rows an expert
+// into 8 x 4096 x 14336).  With one, each lane keeps its row: the trades and the
+// addend together do not fit the registers (157 us against 196 for 64 groups of
+// 1536 rows added in fp32).
+template <int N>
+__device__ __forceinline__ void store_sums(const Set &s, const float (&sum)[N], int64_t at, int lane,
+                                           int rv, int cols, int bytes)
+{
+    if (s.add) {
+        if (lane >= rv)
+            return;
+        const int esz = s.out_f32 ? 4 : 2;
+        const int64_t o = (at + (int64_t)lane * s.ld) * esz;
+        uint8_t *out = static_cast<uint8_t *>(s.out) + o;
+        const uint8_t *add = static_cast<const uint8_t *>(s.add) + o;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {   // 16 columns at a time
+            const float *v = sum + 16 * i;
+            const int end = (cols - 16 * i) * esz;
+            uint32_t w[16];
+            if (s.out_f32) {
+                load_row<2>(add + 64 * i, end, bytes, w);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    w[j] = __float_as_uint(v[j] + __uint_as_float(w[j]));
+                store_row<2>(out + 64 * i, end, bytes, w);
+            } else {
+                load_row<1>(add + 32 * i, end, bytes, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = pack_bf16(v[2 * j] + __uint_as_float(w[j] << 16),
+                                     v[2 * j + 1] + __uint_as_float(w[j] & 0xffff0000u));
+                store_row<1>(out + 32 * i, end, bytes, w);
+            }
+        }
+        return;
+    }
+    const int q = lane & 3, r0 = lane & ~3;
+    if (!s.out_f32) {
+        uint16_t *out = static_cast<uint16_t *>(s.out) + at;
+#pragma unroll
+        for (int i = 0; i < N / 64; ++i) {
+            if (64 * i >= cols)
+                break;
+            uint32_t w[4][8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[k][j] = pack_bf16(sum[64 * i + 16 * k + 2 * j], sum[64 * i + 16 * k + 2 * j + 1]);
+            transpose_blocks(w, lane);
+            const int c = 64 * i + 16 * q;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint16_t *p = out + (int64_t)(r0 + k) * s.ld + c;
+                if (r0 + k >= rv)
+                    continue;
+                if (bytes == 32) {
+                    if (c < cols)
+                        st32(p, w[k]);
+                } else {
+                    if (c < cols)
+                        st16(p, w[k]);
+                    if (c + 8 < cols)
+                        st16(p + 8, w[k] + 4);
+                }
+            }
+        }
+        return;
+    }
+    float *out = static_cast<float *>(s.out) + at;
+#pragma unroll
+    for (int i = 0; i < N / 32; ++i) {
+        if (32 * i >= cols)
+            break;
+        uint32_t w[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[k][j] = __float_as_uint(sum[32 * i + 8 * k + j]);
+        transpose_blocks(w, lane);
+        const int c = 32 * i + 8 * q;
+        if (c >= cols)
+            continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float *p = out + (int64_t)(r0 + k) * s.ld + c;
+            if (r0 + k >= rv)
+                continue;
+            if (bytes == 32) {
+                st32(p, w[k]);
+            } else {
+                st16(p, w[k]);
+                st16(p + 4, w[k] + 4);
+            }
         }
     }
 }
@@ -498,11 +635,6 @@ __device__ __forceinline__ void add_parts(const float4 *from, int64_t step, int 
     }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&h);
-}
 __device__ __forceinline__ uint32_t pack_fp16(float a, float b)
 {
     __half2 h = __floats2half2_rn(a, b);
@@ -1040,47 +1172,9 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                     for (int i = 0; i < BN / 2; i += 32)
                         add_parts(from + 8 * i, part_step, t.parts, sum + i);
                 }
-                if (mine) {
-                    const int c0 = half * (BN / 2), cols = c_end - c0;
-                    const int esz = s.out_f32 ? 4 : 2;
-                    uint8_t *out = static_cast<uint8_t *>(s.out) + (at0 + c0) * esz;
-                    const uint8_t *add = s.add ? static_cast<const uint8_t *>(s.add) +
-                                                     (at0 + c0) * esz
-                                               : nullptr;
-#pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) {   // 16 columns at a time
-                        float *v = sum + 16 * i;
-                        const int end = (cols - 16 * i) * esz;
-                        uint32_t w[16];
-                        if (s.out_f32) {
-                            if (add) {
-                                load_row<2>(add + 64 * i, end, bytes, w);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    w[j] = __float_as_uint(v[j] + __uint_as_float(w[j]));
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    w[j] = __float_as_uint(v[j]);
-                            }
-                            store_row<2>(out + 64 * i, end, bytes, w);
-                        } else {
-                            if (add) {
-                                load_row<1>(add + 32 * i, end, bytes, w);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    w[j] = pack_bf16(v[2 * j] + __uint_as_float(w[j] << 16),
-                                                     v[2 * j + 1] +
-                                                         __uint_as_float(w[j] & 0xffff0000u));
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                            }
-                            store_row<1>(out + 32 * i, end, bytes, w);
-                        }
-                    }
-                }
+                if (rv > 0)
+                    store_sums<BN / 2>(s, sum, at0 - (int64_t)lane * s.ld + half * (BN / 2), lane,
+                                       rv, c_end - half * (BN / 2), bytes);
                 continue;
             }
             bool released = false;
