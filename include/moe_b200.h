@@ -489,7 +489,7 @@ moe_status moe_forward(const moe_config *cfg, const moe_weights *w,
  *
  * bf16 runs on the tensor cores and accumulates in fp32; N and K are multiples
  * of 8 there (16-byte rows, else MOE_ERR_SHAPE) and pointers 16-byte aligned.
- * fp32 runs on the CUDA cores, any N and K.  1 <= G <= 256.  Every call takes a
+ * fp32 runs on the CUDA cores, any N and K.  1 <= G <= 256, N, K <= 2^20.  Every call takes a
  * workspace whose first word is the device status word (cleared by the call),
  * is safe to capture in a CUDA graph, and gives the same bits on every run. */
 

@@ -1194,6 +1194,11 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                     for (int i = 0; i < BN / 64; ++i) {
                         float v[32];
                         tmem_ld32(tq + slot * BN + half * (BN / 2) + 32 * i, v);
+                        if (t.b0 == t.b1) {   // a part of a short contraction may be empty
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = 0.f;
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             part0[(8 * i + j) * 32 + lane] =

@@ -192,7 +192,8 @@ moe_status check_grouped(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t
 {
     if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16)
         return MOE_ERR_DTYPE;
-    if (G < 1 || G > kMaxE || R < 0 || R > INT32_MAX / 2 || N < 1 || K < 1)
+    if (G < 1 || G > kMaxE || R < 0 || R > INT32_MAX / 2 || N < 1 || K < 1 || N > 1 << 20 ||
+        K > 1 << 20)
         return MOE_ERR_SHAPE;
     if (dtype == MOE_DTYPE_BF16 && (N % 8 || K % 8))
         return MOE_ERR_SHAPE;   // 16-byte rows for TMA

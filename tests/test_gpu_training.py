@@ -50,6 +50,7 @@ def within(got, ref, bound, what=""):
 
 SIZES = {
     "one_row": [1],
+    "few_rows": [3, 0, 20, 33, 1, 32],
     "ragged": [0, 1, 127, 128, 129, 0, 300, 15, 16, 17],
     "long": [700, 513, 0, 1030],
     "single": [0, 0, 5],
@@ -108,6 +109,63 @@ def test_grouped_products(sizes, aligned, N, K, dtype):
         s2 = s + 2.0 ** -23 * (r2.abs() + add[g].to(F64).abs())
         within(dWa[g], r2, h * r2.abs() + s2, "dW added")
         within(acc[g], 2 * r, 2.0 ** -22 * r.abs() + 2 * s, "dW accumulated")
+
+
+@pytest.mark.parametrize("sizes,N,K", [([600], 256, 4096), ([5, 40], 136, 8192), ([30, 700], 72, 5000),
+                                       ([9000, 3, 0, 2000], 128, 128), ([3000], 320, 264),
+                                       ([20, 17, 9, 31, 2], 264, 3000)])
+def test_long_contractions_are_cut_and_joined(sizes, N, K):
+    """Few tiles over long contractions: parts of a tile run side by side.  Every
+    run gives the same bits, whichever part is last and whatever the workspace
+    held."""
+    off, rows, R, spans = table(sizes, False)
+    G = len(spans)
+    x, dy = randn(R, K, seed=1), randn(R, N, seed=2)
+    W = randn(G, N, K, seed=3, scale=K ** -0.5)
+    ws = moe.workspace(moe.lib().moe_grouped_workspace_size(1, G, R, N, K), "cuda")
+    results = []
+    for fill in (255, 0, 7):
+        ws.fill_(fill)
+        for _ in range(3):
+            results.append((moe.moe_grouped_matmul(x, W, off, y=torch.zeros_like(dy), ws=ws),
+                            moe.moe_grouped_matmul_dx(dy, W, off, dx=torch.zeros_like(x), ws=ws),
+                            moe.moe_grouped_matmul_dw(dy, x, off, out_dtype=F32, ws=ws)))
+            assert moe.moe_device_status(ws) == 0
+    for r in results[1:]:
+        for a, b in zip(r, results[0]):
+            assert torch.equal(a, b)
+    y, dx, dW = results[0]
+    for g, (lo, hi) in enumerate(spans):
+        a, b, w = x[lo:hi].to(F64), dy[lo:hi].to(F64), W[g].to(F64)
+        r = a @ w.T
+        within(y[lo:hi], r, 2.0 ** -8 * r.abs() + K * 2.0 ** -23 * (a.abs() @ w.abs().T), "y")
+        r = b @ w
+        within(dx[lo:hi], r, 2.0 ** -8 * r.abs() + N * 2.0 ** -23 * (b.abs() @ w.abs()), "dx")
+        r = b.T @ a
+        # summed in accumulators of 512 rows: the truncations do not add up over all of them
+        n = min(hi - lo, 512) + (hi - lo) / 512 + 20
+        within(dW[g], r, 2.0 ** -24 * r.abs() + n * 2.0 ** -23 * (b.abs().T @ a.abs()), "dW")
+
+
+def test_calls_side_by_side_on_two_streams():
+    """Two products on two streams with workspaces of their own give the bits of
+    the same calls in turn."""
+    off, _, R, spans = table([600, 40, 300], False)
+    W = randn(3, 264, 2048, seed=3, scale=1 / 45)
+    xs = [randn(R, 2048, seed=s) for s in (1, 2)]
+    want = [moe.moe_grouped_matmul(x, W, off, y=torch.zeros((R, 264), dtype=BF, device="cuda"))
+            for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        got = []
+        for x, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                y = torch.zeros((R, 264), dtype=BF, device="cuda")
+                got.append(moe.moe_grouped_matmul(x, W, off, y=y))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
 
 
 def test_grouped_products_of_no_rows():
@@ -220,6 +278,9 @@ FFN_CASES = {
     "gelu_pair": (0, [700, 513, 400, 1], 1, 64, 192, 320),
     "swiglu_pair": (1, [129, 800, 0, 650], 2, 192, 320, 128),
     "swiglu_one_token": (1, [1, 0, 0, 0], 3, 64, 64, 64),
+    # long contractions beside a shared expert of one block: parts of cut tiles stay empty
+    "swiglu_long_beside_short": (1, [90, 70, 40, 33], 1, 64, 64, 2048),
+    "gelu_long_beside_short": (0, [90, 70, 40, 33], 1, 64, 64, 4096),
 }
 
 

@@ -22,6 +22,7 @@ def rows_args(dtype=BF16, G=2, R=10, N=64, K=32, x=P, W=P, off=P, rows=None, y=P
     (dict(dtype=2), _abi.MOE_ERR_DTYPE), (dict(G=0), _abi.MOE_ERR_SHAPE),
     (dict(G=257), _abi.MOE_ERR_SHAPE), (dict(R=-1), _abi.MOE_ERR_SHAPE),
     (dict(R=1 << 31), _abi.MOE_ERR_SHAPE), (dict(N=0), _abi.MOE_ERR_SHAPE),
+    (dict(N=(1 << 20) + 8), _abi.MOE_ERR_SHAPE), (dict(K=1 << 21), _abi.MOE_ERR_SHAPE),
     (dict(N=60), _abi.MOE_ERR_SHAPE), (dict(K=33), _abi.MOE_ERR_SHAPE),
     (dict(x=None), _abi.MOE_ERR_NULL), (dict(W=None), _abi.MOE_ERR_NULL),
     (dict(off=None), _abi.MOE_ERR_NULL), (dict(y=None), _abi.MOE_ERR_NULL),
