@@ -489,9 +489,11 @@ moe_status moe_forward(const moe_config *cfg, const moe_weights *w,
  *
  * bf16 runs on the tensor cores and accumulates in fp32; N and K are multiples
  * of 8 there (16-byte rows, else MOE_ERR_SHAPE) and pointers 16-byte aligned.
- * fp32 runs on the CUDA cores, any N and K.  1 <= G <= 256, N, K <= 2^20.  Every call takes a
- * workspace whose first word is the device status word (cleared by the call),
- * is safe to capture in a CUDA graph, and gives the same bits on every run. */
+ * fp32 runs on the CUDA cores, any N and K.  1 <= G <= 256, N, K <= 2^20.  A workspace
+ * serves one call at a time; its contents do not matter, and its first word is
+ * the device status word (cleared by the call).  The grouped products in fp32 do
+ * without (ws NULL).  Every call is safe to capture in a CUDA graph and gives the
+ * same bits on every run. */
 
 /* Workspace bytes of the three grouped products; 0 for invalid arguments. */
 size_t moe_grouped_workspace_size(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K);

@@ -214,6 +214,14 @@ moe_status check_ws(const void *ws, size_t bytes, size_t need)
     return bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
+// fp32: nothing waits on the device, and the workspace is only the status word
+moe_status check_grouped_ws(int32_t dtype, const void *ws, size_t bytes)
+{
+    if (dtype == MOE_DTYPE_F32 && !ws)
+        return MOE_OK;
+    return check_ws(ws, bytes, grouped_bytes(dtype));
+}
+
 moe_status rows_call(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K, const void *in,
                      const void *W, const int32_t *offsets, const int32_t *rows, void *out,
                      void *ws, size_t ws_bytes, moe_stream_t stream, bool back)
@@ -226,12 +234,12 @@ moe_status rows_call(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K, 
     const uintptr_t al = dtype == MOE_DTYPE_BF16 ? 16 : 4;
     if (!aligned(in, al) || !aligned(W, al) || !aligned(out, al))
         return MOE_ERR_ALIGN;
-    if ((st = check_ws(ws, ws_bytes, grouped_bytes(dtype))) != MOE_OK)
+    if ((st = check_grouped_ws(dtype, ws, ws_bytes)) != MOE_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Table t{offsets, rows, (int)R};
     if (R == 0)
-        return cuda_status(clear_word(ws, s));
+        return ws ? cuda_status(clear_word(ws, s)) : MOE_OK;
     if (dtype == MOE_DTYPE_BF16)
         return cuda_status(rows_tc(t, G, R, N, K, in, W, out, back, ws, s));
     Simt p = simt_rows(t, RAGGED_M, G, 0, N, K, static_cast<const float *>(in), 0,
@@ -494,7 +502,7 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
     const uintptr_t al = dtype == MOE_DTYPE_BF16 ? 16 : 4;
     if (!aligned(dy, al) || !aligned(x, al) || !aligned(dW, al) || !aligned(add, al))
         return MOE_ERR_ALIGN;
-    if ((st = check_ws(ws, ws_bytes, grouped_bytes(dtype))) != MOE_OK)
+    if ((st = check_grouped_ws(dtype, ws, ws_bytes)) != MOE_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Table t{offsets, rows, (int)R};

@@ -75,6 +75,15 @@ def _ws(nbytes, ws, device):
     return workspace(nbytes, device) if ws is None else ws
 
 
+def _grouped_ws(sizes, ws, device):
+    """(workspace, bytes): the fp32 products do without."""
+    if ws is None:
+        if sizes[0] == DTYPE_F32:
+            return None, 0
+        ws = workspace(lib().moe_grouped_workspace_size(*sizes), device)
+    return ws, ws.numel()
+
+
 def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
     """y[r] = W[g] x[r] for the rows r of each group g: x [R, K], W [G, N, K],
     offsets [G + 1] (and rows [G]) int32.  Rows of no group are not written."""
@@ -84,8 +93,8 @@ def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
     if y is None:
         y = torch.empty(shape, dtype=x.dtype, device=x.device)
     _is(y, shape, x.dtype, "y")
-    ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, x.device)
-    check(lib().moe_grouped_matmul(*sizes, *_ptrs(x, W, offsets, rows, y, ws), ws.numel(),
+    ws, nbytes = _grouped_ws(sizes, ws, x.device)
+    check(lib().moe_grouped_matmul(*sizes, *_ptrs(x, W, offsets, rows, y, ws), nbytes,
                                    _stream()), "moe_grouped_matmul")
     return y
 
@@ -98,8 +107,8 @@ def moe_grouped_matmul_dx(dy, W, offsets, rows=None, dx=None, ws=None):
     if dx is None:
         dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
     _is(dx, shape, dy.dtype, "dx")
-    ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, dy.device)
-    check(lib().moe_grouped_matmul_dx(*sizes, *_ptrs(dy, W, offsets, rows, dx, ws), ws.numel(),
+    ws, nbytes = _grouped_ws(sizes, ws, dy.device)
+    check(lib().moe_grouped_matmul_dx(*sizes, *_ptrs(dy, W, offsets, rows, dx, ws), nbytes,
                                       _stream()), "moe_grouped_matmul_dx")
     return dx
 
@@ -120,9 +129,9 @@ def moe_grouped_matmul_dw(dy, x, offsets, rows=None, add=None, dW=None, out_dtyp
         dW = torch.empty(shape, dtype=out_dtype, device=dy.device)
     _is(dW, shape, out_dtype, "dW")
     _is(add, shape, out_dtype, "add")
-    ws = _ws(lib().moe_grouped_workspace_size(*sizes), ws, dy.device)
+    ws, nbytes = _grouped_ws(sizes, ws, dy.device)
     check(lib().moe_grouped_matmul_dw(*sizes, *_ptrs(dy, x, offsets, rows), _code(dW, "dW"),
-                                      *_ptrs(add, dW, ws), ws.numel(), _stream()),
+                                      *_ptrs(add, dW, ws), nbytes, _stream()),
           "moe_grouped_matmul_dw")
     return dW
 
@@ -136,7 +145,7 @@ def moe_combine_backward(cfg: MoeConfig, dy, Y_perm, gates, topk, pos, keep, off
     if dY_perm is None:
         dY_perm = torch.empty((R, d), dtype=dt, device=dy.device)
     if dgates is None:
-        dgates = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+        dgates = torch.empty_like(gates, dtype=torch.float32)
     for t, shape, dtype, what in ((dy, (T, d), dt, "dy"), (Y_perm, (R, d), dt, "Y_perm"),
                                   (dY_perm, (R, d), dt, "dY_perm"),
                                   (gates, (T, k), torch.float32, "gates"),

@@ -45,6 +45,15 @@ def test_weight_gradient_checks_its_arguments(kw, status):
     assert moe.lib().moe_grouped_matmul_dw(*a.values(), None) == status
 
 
+def test_fp32_products_take_no_workspace():
+    """Only bf16 needs one: with none, the fp32 call gets past the check (and, no
+    rows, launches nothing)."""
+    L = moe.lib()
+    assert L.moe_grouped_matmul(*rows_args(dtype=F32, R=0, ws=None, nb=0)) == _abi.MOE_OK
+    assert L.moe_grouped_matmul_dx(*rows_args(dtype=F32, R=0, ws=None, nb=0)) == _abi.MOE_OK
+    assert L.moe_grouped_matmul(*rows_args(dtype=F32, R=0, ws=P, nb=8)) == _abi.MOE_ERR_WORKSPACE
+
+
 def test_workspace_sizes():
     L = moe.lib()
     assert L.moe_grouped_workspace_size(BF16, 4, 100, 64, 64) >= 256
