@@ -28,11 +28,10 @@ struct Set {
     // seg_grouped both operands' group is i / period.
     CUtensorMap a[2], b[2];
     CUtensorMap a_few;           // a[0] in boxes of 32 rows, if has_few (ONE_128, one segment)
-    CUtensorMap c[2];            // EPI_NS: out and out2, made at launch (c_map: valid)
     CUtensorMap b3;              // EPI_SWIGLU: W3 (b[0] = W1, b[1] = W2)
     int mode, groups, ent0;      // ent0: first entry of the tile table
     int M, N, K;                 // output rows (not RAGGED_M), columns, contraction (not RAGGED_K)
-    int segs, period, seg_grouped, has_few, c_map;
+    int segs, period, seg_grouped, has_few;
     int a_grouped, b_grouped;    // 1: the operand has one matrix per group
     int a_wide, b_wide;          // 1: one box is a whole stage (all segments')
     int sym;                     // 1: out is symmetric; only tiles on or below the diagonal

@@ -35,11 +35,10 @@
 // adds the parts up in their order and stores the rows, so the result does not
 // depend on who was last.  split_plan() weighs the rounds saved against that.
 //
-// Output rows of ragged groups go from registers to memory, each masked by the
-// group's end: rows behind it are neither written nor read.  The stacks' tiles go
-// through 2 KB of shared memory a warp and out by TMA, which clips them at the
-// matrix (weight gradients measured 1.2 times as long that way: a warp waits for
-// its one tile to be read before the next piece).
+// Output rows go from registers to memory, each masked by the group's end: rows
+// behind it are neither written nor read.  (Out by TMA through the 2 KB a warp
+// that the ring leaves, weight gradients took 1.2 times as long: a warp waits for
+// its piece to be read before the next.)
 //
 // Roles: warp 0 loads, warp 1 issues the MMAs (and owns TMEM), the last eight
 // are the epilogue (warp w reads TMEM lanes 32 (w mod 4) .. +31, the first four
@@ -88,7 +87,7 @@ struct Shape {
     static constexpr int BK = 64 * KSUB;
     static constexpr int MN_BLOCK = BK * 128;            // 64 columns of an MN-major stage
     static constexpr int OFF_B = STAGES * KSUB * A_BYTES;
-    static constexpr bool STAGED = EPI == EPI_NS;   // output by TMA
+    static constexpr bool STAGED = EPI == EPI_NS;   // rows of odd pitch go through shared memory
     static constexpr int OFF_STG = OFF_B + STAGES * KSUB * B_BYTES;
     static constexpr int OFF_BAR = OFF_STG + (STAGED ? EPI_WARPS * STG_WARP : 0);
     static constexpr int OFF_TAB = OFF_BAR + 256;
@@ -354,23 +353,6 @@ __device__ __forceinline__ void st16(void *p, const uint32_t *w)
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 32 columns of packed 16-bit values of this lane's row, the first cv of them (a
-// multiple of 8) to dst.  bytes: what every row is aligned to.
-__device__ __forceinline__ void store16(const uint32_t *w, uint16_t *dst, int cv, int bytes)
-{
-    if (bytes == 32) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            if (16 * c < cv)
-                st32(dst + 16 * c, w + 8 * c);
-    } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (8 * c < cv)
-                st16(dst + 8 * c, w + 4 * c);
-    }
-}
-
 __device__ __forceinline__ void ld32(const void *p, uint32_t *w)
 {
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -418,13 +400,14 @@ __device__ __forceinline__ void store_row(uint8_t *p, int end, int bytes, const 
     }
 }
 
-// 4 x 4 transpose of 32-byte blocks over four neighbouring lanes: lane q of them
-// holds row q's blocks 0..3 before, block q of rows 0..3 after.
-__device__ __forceinline__ void transpose_blocks(uint32_t (&w)[4][8], int lane)
+// 4 x 4 transpose of blocks of W words over four neighbouring lanes: lane q of
+// them holds row q's blocks 0..3 before, block q of rows 0..3 after.
+template <int W>
+__device__ __forceinline__ void transpose_blocks(uint32_t (&w)[4][W], int lane)
 {
     const bool b0 = lane & 1, b1 = lane & 2;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < W; ++j) {
 #pragma unroll
         for (int k = 0; k < 4; k += 2) {   // blocks k, k + 1 with the odd/even neighbour
             const uint32_t o = __shfl_xor_sync(0xffffffffu, b0 ? w[k][j] : w[k + 1][j], 1);
@@ -442,6 +425,26 @@ __device__ __forceinline__ void transpose_blocks(uint32_t (&w)[4][8], int lane)
                 w[k + 2][j] = o;
         }
     }
+}
+
+// 32 columns of packed 16-bit values of this lane's row: four lanes trade 16-byte
+// blocks, so that a row's 64 bytes leave in one instruction.  out: row 0 of the
+// warp, first column; rv rows and cv columns (a multiple of 8) are stored.
+__device__ __forceinline__ void store_traded(const uint32_t *v, uint16_t *out, int64_t ld, int lane,
+                                             int rv, int cv)
+{
+    uint32_t w[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[k][j] = v[4 * k + j];
+    transpose_blocks(w, lane);
+    const int r0 = lane & ~3, c = 8 * (lane & 3);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (r0 + k < rv && c < cv)
+            st16(out + (r0 + k) * ld + c, w[k]);
 }
 
 // This lane's row of N sums (plus the addend) to fp32 or bf16.  at: element
@@ -548,31 +551,8 @@ __device__ __forceinline__ void store_sums(const Set &s, const float (&sum)[N], 
     }
 }
 
-// 32 rows of 64 bytes, one a lane, through the staging tile to (c0, c1, c2) of
-// the map.  The tile is written again once the copy before has read it.
-__device__ __forceinline__ void store_box(const CUtensorMap *map, uint8_t *stg, int lane,
-                                          const uint32_t *w, int c0, int c1, int c2)
-{
-    if (lane == 0)
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::
-                         "l"(reinterpret_cast<uint64_t>(map)),
-                     "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(stg))
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-}
-
-// The same tile to rows of any alignment: a warp writes one row's 32 values at a
-// time.  out: column 0 of row 0; rv rows and cv columns are stored.
+// The same to rows of any alignment, through a tile in shared memory: a warp
+// writes one row's 32 values at a time.  out: column 0 of row 0; rv rows and cv columns are stored.
 __device__ __forceinline__ void store_odd(uint8_t *stg, int lane, const uint32_t *w, uint16_t *out,
                                           int64_t ld, int rv, int cv)
 {
@@ -1097,10 +1077,10 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                 break;
             tc_fence_after();
             const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
-            const int64_t row = m + lane + (s.mode == RAGGED_M ? t.row0 : 0);
+            // element (first row of the warp, first column of the tile) of the output
+            const int64_t row = m + (s.mode == RAGGED_M ? t.row0 : 0);
             const int64_t at0 = (s.mode == RAGGED_M ? 0 : (int64_t)t.g * s.out_group) +
                                 row * s.ld + t.n0;
-            const bool mine = lane < rv;
             const int bytes = s.bytes;
             // a cut tile's parts: 32 rows x BN / 2 columns of this warp, 4 columns of
             // a lane together
@@ -1173,7 +1153,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                         add_parts(from + 8 * i, part_step, t.parts, sum + i);
                 }
                 if (rv > 0)
-                    store_sums<BN / 2>(s, sum, at0 - (int64_t)lane * s.ld + half * (BN / 2), lane,
+                    store_sums<BN / 2>(s, sum, at0 + half * (BN / 2), lane,
                                        rv, c_end - half * (BN / 2), bytes);
                 continue;
             }
@@ -1243,10 +1223,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             w[i / 2] = pack_bf16(h[0], h[1]);
                             g[i / 2] = pack_bf16(du[0], du[1]);
                         }
-                        if (mine) {
-                            store16(w, static_cast<uint16_t *>(s.out) + at, cv, bytes);
-                            store16(g, static_cast<uint16_t *>(s.out2) + at, cv, bytes);
-                        }
+                        store_traded(w, static_cast<uint16_t *>(s.out) + at, s.ld, lane, rv, cv);
+                        store_traded(g, static_cast<uint16_t *>(s.out2) + at, s.ld, lane, rv, cv);
                     } else {
                         float x3[32];
                         tmem_ld32(tu + BN, x3);
@@ -1267,11 +1245,9 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             g[i / 2] = pack_bf16(du[0], du[1]);
                             k[i / 2] = pack_bf16(dv[0], dv[1]);
                         }
-                        if (mine) {
-                            store16(w, static_cast<uint16_t *>(s.out) + at, cv, bytes);
-                            store16(g, static_cast<uint16_t *>(s.out2) + at, cv, bytes);
-                            store16(k, static_cast<uint16_t *>(s.out3) + at, cv, bytes);
-                        }
+                        store_traded(w, static_cast<uint16_t *>(s.out) + at, s.ld, lane, rv, cv);
+                        store_traded(g, static_cast<uint16_t *>(s.out2) + at, s.ld, lane, rv, cv);
+                        store_traded(k, static_cast<uint16_t *>(s.out3) + at, s.ld, lane, rv, cv);
                     }
                 } else {
                     if (t.parts > 1) {
@@ -1284,8 +1260,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                        if (mine)
-                            store16(w, static_cast<uint16_t *>(s.out) + at, cv, bytes);
+                        store_traded(w, static_cast<uint16_t *>(s.out) + at, s.ld, lane, rv, cv);
                     } else if constexpr (EPI == EPI_NS) {
                         float alpha = s.alpha, beta = s.beta;
                         if (s.scale) {
@@ -1316,16 +1291,18 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                            if (s.c_map)
-                                store_box(&s.c[0], stg, lane, w, t.n0 + c, m, t.g);
+                            if (bytes >= 16)
+                                store_traded(w, hi, s.ld, lane, rv, cv);
                             else
-                                store_odd(stg, lane, w, hi - (int64_t)lane * s.ld, s.ld, rv, cv);
+                                store_odd(stg, lane, w, hi, s.ld, rv, cv);
                             continue;
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[i] = pack_fp16(v[2 * i], v[2 * i + 1]);
-                        store_box(&s.c[0], stg, lane, w, t.n0 + c, m, t.g);
+                        // columns past N up to the pitch's multiple of 8 are written too
+                        const int cw = (cv + 7) & ~7;
+                        store_traded(w, hi, s.ld, lane, rv, cw);
                         if (s.out2) {
                             uint32_t lw[16];
 #pragma unroll
@@ -1333,7 +1310,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                                 const float2 f = unpack_fp16(w[i]);
                                 lw[i] = pack_fp16(v[2 * i] - f.x, v[2 * i + 1] - f.y);
                             }
-                            store_box(&s.c[1], stg, lane, lw, t.n0 + c, m, t.g);
+                            store_traded(lw, static_cast<uint16_t *>(s.out2) + at, s.ld, lane, rv,
+                                         cw);
                         }
                         if (s.sym && t.n0 + BN <= t.m0)
                             store_mirror(w,
@@ -1346,11 +1324,6 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
             }
             if (!released)
                 release();
-        }
-        if (S::STAGED) {
-            if (lane == 0)
-                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            __syncwarp();
         }
     }
 
@@ -1412,10 +1385,6 @@ cudaError_t launch_one(const Params &p, cudaStream_t s)
 
 constexpr int kBnAct = 128;
 
-}  // namespace
-
-namespace {
-
 // [groups, rows, cols] 2-byte elements, row pitch ld, as (64, rows, cols / 64,
 // groups) with boxes of `blocks` blocks of 64 columns (wide), or as (cols, rows,
 // 1, groups) with boxes of 64 columns.
@@ -1436,14 +1405,6 @@ bool map_4d(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [groups, rows, cols] of 2-byte elements, boxes of 32 rows x 64 bytes
-bool map_out(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-             int64_t groups, int64_t group_stride)
-{
-    return make_map(m, base, cols, rows, groups, ld * 2, group_stride * 2, 32, 32,
-                    CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
@@ -1488,19 +1449,6 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream
                               reinterpret_cast<uint64_t>(v.base);
         v.base_bytes = base % 32 == 0 ? 32 : 16;
         ents += v.groups;
-        v.c_map = 0;
-        if (epi == EPI_NS) {
-            // outputs by TMA: 32 rows of 64 bytes; any matrix whose rows start on 16 bytes
-            if (v.bytes >= 16) {
-                v.c_map = 1;
-                if (!map_out(&v.c[0], v.out, v.M, v.N, v.ld, v.groups, v.out_group) ||
-                    (v.out2 &&
-                     !map_out(&v.c[1], v.out2, v.M, v.N, v.ld, v.groups, v.out_group)))
-                    return cudaErrorInvalidValue;
-            } else if (!v.out_bf16) {
-                return cudaErrorInvalidValue;
-            }
-        }
     }
     if (ents > kEntries)
         return cudaErrorInvalidValue;
