@@ -62,9 +62,19 @@ void set_cut(Params &p, void *ws)
     p.partial_bytes = kPartialBytes;
 }
 
-// Products over short groups use 128-row tiles: a 256-row tile would mostly
-// compute rows of nobody.
-Tiles row_tiles(int64_t rows, int64_t groups) { return rows >= 384 * groups ? PAIR_256 : ONE_128; }
+// Tiles for `rows` rows in `groups` groups of about the same length, n columns.
+// A round of tiles costs its loads, 64 KB a stage and SM either way, so 256 x 256
+// on SM pairs take over where they need fewer rounds than 128 x 128: past 128
+// rows a group (8 x 200 rows through 4096 x 4096: 70 us against 92; 8 x 100: 68
+// against 61).  The hidden gradients' single-SM tiles load 96 KB for 64.
+Tiles row_tiles(int64_t rows, int64_t groups, int64_t n, bool hidden)
+{
+    const int64_t each = ceil_div(rows, groups), sms = device_sms();
+    const int64_t pair = ceil_div(groups * ceil_div(each, 256) * ceil_div(n, hidden ? 128 : 256),
+                                  sms / 2);
+    const int64_t one = ceil_div(groups * ceil_div(each, 128) * ceil_div(n, 128), sms);
+    return (hidden ? 2 * pair < 3 * one : pair < one) ? PAIR_256 : ONE_128;
+}
 // Weight gradients: 256 x 256 tiles once the matrix fills them.
 Tiles dw_tiles(int64_t M, int64_t N) { return M >= 256 && N >= 256 ? PAIR_256 : ONE_128; }
 
@@ -74,7 +84,7 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
 {
     Params p = tc_params(t, status, true);
     // few rows a group: the weights' bytes are the work
-    const Tiles tiles = R <= 24ll * G ? ONE_32 : row_tiles(R, G);
+    const Tiles tiles = R <= 24ll * G ? ONE_32 : row_tiles(R, G, back ? K : N, false);
     Set &a = p.set[0];
     p.nsets = 1;
     a.mode = RAGGED_M;
@@ -292,14 +302,15 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     const int64_t R = t.n_rows;
     const int d = c.d, F = c.d_ff, E = c.E, S = c.n_shared, Fs = c.d_ff_shared, T = c.T;
     const bool swiglu = c.act == MOE_ACT_SWIGLU, shared = S > 0 && T > 0;
-    const Tiles tiles = row_tiles((int64_t)T * c.k, E);
+    const Tiles hid = row_tiles((int64_t)T * c.k, E, F, true);
+    const Tiles tiles = row_tiles((int64_t)T * c.k, E, d, false);
     const Epi epi = swiglu ? EPI_SWIGLU : EPI_GELU;
     cudaError_t e;
     bool ok = true;
 
     // h, du, dv from x and dy
     Params p = tc_params(t, status, true);
-    const int ubox = b_box(epi, tiles), ask = stage_k(epi, tiles);   // widths: multiples of 64
+    const int ubox = b_box(epi, hid), ask = stage_k(epi, hid);   // widths: multiples of 64
     auto act_set = [&](Set &v, int mode, int groups, int64_t rows, int cols, const void *in,
                        const void *dout, const void *w1, const void *w3, const void *w2, void *h,
                        void *du, void *dv) {
@@ -319,7 +330,7 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
         ok &= map_k(&v.a[0], dout, rows, d, d, 1, 0, 128, ask, true);
         ok &= map_k(&v.a[1], in, rows, d, d, 1, 0, 128, ask, true);
         ok &= map_k(&v.b[0], w1, cols, d, d, groups, (int64_t)cols * d, ubox, ask, true);
-        ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d, ask, dh_box(tiles),
+        ok &= map_mn(&v.b[1], w2, d, cols, cols, groups, (int64_t)cols * d, ask, dh_box(hid),
                      true);
         if (swiglu)
             ok &= map_k(&v.b3, w3, cols, d, d, groups, (int64_t)cols * d, ubox, ask, true);
@@ -332,7 +343,7 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     }
     if (!ok)
         return cudaErrorInvalidValue;
-    if ((e = launch_tc(p, epi, A_K_B_K, tiles, s)) != cudaSuccess)
+    if ((e = launch_tc(p, epi, A_K_B_K, hid, s)) != cudaSuccess)
         return e;
 
     // dx = du W1 (+ dv W3); shared: summed over the experts in the accumulator
