@@ -76,6 +76,9 @@ struct Shape {
     static constexpr int FIRST_EPI = EPI == EPI_DW ? 3 : 2;   // first of the epilogue warps
     static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
     static constexpr int MMA_M = 128 * CTAS;
+    // epilogue warps of a CTA that have rows, and floats of a cut tile's part
+    static constexpr int ROW_WARPS = 2 * (AR / 32);
+    static constexpr int PART = BM * BN;
     // accumulator columns of the widest B tile (ACT: u, with v beside it)
     static constexpr int BNB = EPI == EPI_SWIGLU ? 2 * BN : BN;
     static constexpr int B_ROWS = BNB / CTAS;            // B rows of one CTA
@@ -758,7 +761,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                 k /= s.groups;
             }
             pl = split_plan<CTAS>(base, s.segs * ((k + S::BK - 1) / S::BK), units,
-                                  p.partial_bytes / (BM * BN * 4), lane);
+                                  p.partial_bytes / (S::PART * 4), lane);
         }
         if (lane == 0) {
             tstart[p.entries] = base;
@@ -1084,12 +1087,12 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
             const int bytes = s.bytes;
             // a cut tile's parts: 32 rows x BN / 2 columns of this warp, 4 columns of
             // a lane together
-            const int wid = (int)rank * EPI_WARPS + half * 4 + q;
-            const int64_t part_step = (int64_t)CTAS * EPI_WARPS * (BN / 8) * 32;
+            const int wid = (int)rank * S::ROW_WARPS + half * (AR / 32) + q;
+            const int64_t part_step = S::PART / 4;
             float4 *part0 = reinterpret_cast<float4 *>(p.partial) +
                             ((int64_t)t.cut * t.parts + t.part) * part_step +
                             (int64_t)wid * (BN / 8) * 32;
-            unsigned long long *count = p.counters + t.cut * (CTAS * EPI_WARPS) + wid;
+            unsigned long long *count = p.counters + t.cut * (CTAS * S::ROW_WARPS) + wid;
             if constexpr (EPI == EPI_DW) {
                 float sum[BN / 2];
                 if (t.b0 == t.b1) {   // nothing was accumulated: an empty group's sum
@@ -1353,6 +1356,9 @@ cudaError_t launch_one(const Params &p, cudaStream_t s)
     // mn_box_rows: the rows of a stage
     static_assert(S::BK == (CTAS == 1 && EPI == EPI_SWIGLU ? 64 : 128), "stage");
     static_assert(S::DH_COL + 2 * BN <= 512 || !S::ACT, "TMEM");
+    // the counters of the most tiles that are cut at a time
+    static_assert(kPartialBytes / (S::PART * 4) / 2 * CTAS * S::ROW_WARPS * 8 <= kCounterBytes,
+                  "counters");
     auto kern = grouped_kernel<CTAS, BN, A_MN, B_MN, EPI, AR>;
     cudaError_t err = raise_smem_limit((const void *)kern, S::SMEM);
     if (err != cudaSuccess)

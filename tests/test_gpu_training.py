@@ -554,3 +554,24 @@ def test_training_step_captured_and_replayed():
                 assert torch.equal(a, b)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(other[1], want[1])
+
+
+@pytest.mark.parametrize("G,N,K", [(7, 2048, 17280), (1, 9728, 24576)])
+def test_parts_of_few_row_tiles_stay_inside_the_workspace(G, N, K):
+    """Around a hundred tiles of 32 rows over a long contraction are cut into more
+    parts than tiles of 128 rows could be: nothing is written behind the
+    workspace, and the rows are right."""
+    R = 5 * G
+    off = ints([5 * g for g in range(G + 1)])
+    x = randn(R, K, seed=1)
+    W = randn(G, N, K, seed=3, scale=K ** -0.5)
+    need = moe.lib().moe_grouped_workspace_size(1, G, R, N, K)
+    buf = moe.workspace(need + (96 << 20), "cuda")
+    buf.fill_(165)
+    y = moe.moe_grouped_matmul(x, W, off, ws=buf[:need])
+    assert moe.moe_device_status(buf[:need]) == 0
+    assert (buf[need:] == 165).all()
+    for g in range(G):
+        a, w = x[5 * g:5 * g + 5].to(F64), W[g].to(F64)
+        r = a @ w.T
+        within(y[5 * g:5 * g + 5], r, 2.0 ** -8 * r.abs() + K * 2.0 ** -23 * (a.abs() @ w.abs().T))
