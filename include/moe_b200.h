@@ -588,8 +588,8 @@ size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t
  *   [E, m, n] bf16.  coeffs (host): a, b, c; they must keep the singular values
  *   below 2.8 and those of b A + c A A below 16, as 3.4445, -4.775, 2.0315 or
  *   1.5, -0.5, 0 do (fp16 intermediates).  1 <= E <= 1024, m, n <= 2^20, 1 <=
- *   steps <= 32.  A matrix of zeros gives zeros; one with an infinity or NaN
- *   gives NaN, in its own update only.
+ *   steps <= 32.  A matrix of zeros gives zeros (NaN when eps is 0); one with an
+ *   infinity or NaN gives NaN, in its own update only.
  * The products take fp16 operands (X itself is held as two fp16 terms): the
  * result is that of 64-bit arithmetic within about 2e-3 (relative, 2-norm), then
  * rounded to bf16.

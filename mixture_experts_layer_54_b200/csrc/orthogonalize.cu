@@ -71,9 +71,14 @@ __device__ __forceinline__ void load8(const T *p, int n, bool vec, float *f)
     }
 }
 
+// Whether a sum of squares taken in fp32 can be wrong: some overflowed, or the
+// sum is so small that those which vanished (2^-149 each) could matter.
+__device__ __forceinline__ bool squares_outside(double v) { return !(v >= 1e-20 && v <= 1e38); }
+
 // Sums of squares of `parts` slices of each matrix (fp32 in a thread, then
 // double over the block; fixed order).  Four 8-element pieces of a thread are
-// in flight at a time.
+// in flight at a time.  A slice whose squares leave fp32's range is summed again
+// in double.
 template <typename T>
 __global__ void __launch_bounds__(256)
     square_sums_kernel(const T *G, int64_t mn, int parts, bool vec, double *out)
@@ -99,18 +104,34 @@ __global__ void __launch_bounds__(256)
                 acc[u] = fmaf(f[u][j], f[u][j], acc[u]);
     }
     __shared__ double part[8];
-    double v = (double)acc[0] + acc[1] + acc[2] + acc[3];
+    __shared__ int again;
+    auto block_sum = [&](double v) {   // thread 0's answer is the block's
 #pragma unroll
-    for (int s = 16; s; s >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, s);
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = v;
+        for (int s = 16; s; s >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, s);
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 1; i < 8; ++i)
+                v += part[i];
+        return v;
+    };
+    double v = block_sum((double)acc[0] + acc[1] + acc[2] + acc[3]);
+    if (threadIdx.x == 0)
+        again = squares_outside(v);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 8; ++i)
-            v += part[i];
-        out[e * kMaxParts + blockIdx.x] = v;
+    if (again) {
+        v = 0;
+        for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < mn; i += step)
+            for (int64_t j = i; j < i + 8 && j < mn; ++j) {
+                const double x = (double)to_f<T>(g[j]);
+                v += x * x;
+            }
+        v = block_sum(v);
     }
+    if (threadIdx.x == 0)
+        out[e * kMaxParts + blockIdx.x] = v;
 }
 
 // X = G 2^k as one or two fp16 terms, 2^k the power of two that brings |G| + eps
@@ -124,7 +145,7 @@ __global__ void __launch_bounds__(256)
     pdl_wait();
     pdl_trigger();
     const int e = blockIdx.y;
-    __shared__ float s_mul;
+    __shared__ float s_mul[2];   // 2^k as two factors: k may pass fp32's exponents
     if (threadIdx.x < 32) {
         double v = 0;
         for (int i = threadIdx.x; i < parts; i += 32)
@@ -134,21 +155,23 @@ __global__ void __launch_bounds__(256)
             v += __shfl_xor_sync(0xffffffffu, v, s);
         if (threadIdx.x == 0) {
             const double norm = sqrt(v) + (double)eps;
-            double mul = 1.0, sc = norm;   // zero with eps = 0: 0 / 0 as the formula has it
+            double sc = norm;   // zero with eps = 0: 0 / 0 as the formula has it
+            int k = 0;
             if (isfinite(norm) && norm > 0) {
-                const int k = min(max(13 - (int)ceil(log2(norm)), -126), 126);
-                mul = exp2((double)k);
-                sc = mul * norm;
+                k = 13 - (int)ceil(log2(norm));
+                sc = exp2((double)k) * norm;
             } else if (!isfinite(norm)) {
                 sc = nan("");   // an infinity or NaN in G: the whole update is NaN
             }
-            s_mul = (float)mul;
+            const int k0 = min(max(k, -126), 126);
+            s_mul[0] = (float)exp2((double)k0);
+            s_mul[1] = (float)exp2((double)(k - k0));
             if (blockIdx.x == 0)
                 scale[e] = (float)sc;
         }
     }
     __syncthreads();
-    const float mul = s_mul;
+    const float mul = s_mul[0], mul2 = s_mul[1];
     const int cpr = (int)(ld / 8);
     const int64_t chunks = (int64_t)m * cpr;
     const bool flat = n == ld;
@@ -178,7 +201,7 @@ __global__ void __launch_bounds__(256)
             uint32_t h[4], l[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float x0 = f[u][2 * j] * mul, x1 = f[u][2 * j + 1] * mul;
+                const float x0 = f[u][2 * j] * mul * mul2, x1 = f[u][2 * j + 1] * mul * mul2;
                 const __half2 a = __floats2half2_rn(x0, x1);
                 const float2 b = __half22float2(a);
                 const __half2 d = __floats2half2_rn(x0 - b.x, x1 - b.y);

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     __shared__ int abort_flag;
     __shared__ double part[THREADS / 32];
     __shared__ float s_mul, s_over;
+    __shared__ int again;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar = smem_u32(&bar_mem);
     const Ctl ctl{&abort_flag, s.status, 2000000000ull};
@@ -165,18 +166,41 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
         for (int u = 0; u < 4; ++u)
             acc[u] = fmaf(f[u], f[u], acc[u]);
     }
-    double v = (double)acc[0] + acc[1] + acc[2] + acc[3];
+    auto warp_sums = [&](double v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0)
-        part[warp] = v;
+        for (int o = 16; o; o >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0)
+            part[warp] = v;
+    };
+    auto block_sum = [&]() {
+        double v = part[0];
+        for (int i = 1; i < THREADS / 32; ++i)
+            v += part[i];
+        return v;
+    };
+    warp_sums((double)acc[0] + acc[1] + acc[2] + acc[3]);
     tc_fence_before();
     __syncthreads();   // also: shared memory zeroed, barrier and TMEM ready
     tc_fence_after();
+    double v = 0;
     if (tid == 0) {
-        for (int i = 1; i < THREADS / 32; ++i)
-            v += part[i];
+        v = block_sum();
+        again = !(v >= 1e-20 && v <= 1e38);   // some squares may have left fp32's range
+    }
+    __syncthreads();
+    if (again) {
+        double w = 0;
+        for (int i = tid; i < mn; i += THREADS) {
+            const double x = (double)as_float<T>(G[i]);
+            w += x * x;
+        }
+        warp_sums(w);
+        __syncthreads();
+        if (tid == 0)
+            v = block_sum();
+    }
+    if (tid == 0) {
         const double norm = sqrt(v) + (double)s.eps;
         // G times a power of two near kSX / |G| (exact), then the rest of the factor
         double mul = 1.0;

@@ -244,6 +244,8 @@ def moe_orthogonalize(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), scale=1.0, e
     if U is None:
         U = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
     _is(U, G.shape, torch.bfloat16, "U")
+    if len(coeffs) != 3:
+        raise ValueError(f"coeffs are a, b, c, not {len(coeffs)} numbers")
     c = (ctypes.c_float * 3)(*coeffs)
     ws = _ws(moe_orthogonalize_workspace_size(E, m, n, steps), ws, G.device)
     g, u, w = _ptrs(G, U, ws)
