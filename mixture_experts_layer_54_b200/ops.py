@@ -20,18 +20,16 @@ def moe_config(shape=None, **kw) -> MoeConfig:
     """Build the C config from any object with the layer's attributes
     (T, d, E, k, d_ff, act, dtype, cf, and optionally n_shared, d_ff_shared,
     score, renorm, priority) and/or keyword overrides."""
-    def get(name, default=None):
+    def look(name, default=None):
         if name in kw:
             return kw[name]
-        if shape is not None and hasattr(shape, name):
-            return getattr(shape, name)
-        return default
+        return getattr(shape, name, default)
+    get = kw.get if shape is None else look
     cf = get("cf", get("capacity_factor", 1.0))
-    return MoeConfig(T=get("T"), d=get("d"), E=get("E"), k=get("k"), d_ff=get("d_ff"),
-                     n_shared=get("n_shared", 0), d_ff_shared=get("d_ff_shared", 0),
-                     act=get("act", 0), score=get("score", 0), renorm=get("renorm", -1),
-                     dtype=get("dtype", DTYPE_BF16), priority=get("priority", 0),
-                     capacity_factor=float(cf))
+    # in the order of the structure's fields
+    return MoeConfig(get("T"), get("d"), get("E"), get("k"), get("d_ff"), get("n_shared", 0),
+                     get("d_ff_shared", 0), get("act", 0), get("score", 0), get("renorm", -1),
+                     get("dtype", DTYPE_BF16), get("priority", 0), float(cf))
 
 
 def _p(t):

@@ -11,7 +11,7 @@ from dataclasses import dataclass
 import torch
 
 from ._abi import MoeConfig, check, lib
-from .ops import DTYPE_BF16, DTYPE_F32, _p, _tdtype, moe_validate, workspace
+from .ops import DTYPE_BF16, DTYPE_F32, _p, _tdtype, moe_validate
 
 _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
@@ -61,6 +61,13 @@ def _is(t, shape, dtype, what):
                          f"{dtype} {tuple(shape)} wanted")
 
 
+def _fit(specs):
+    """_is of every (tensor, shape, dtype, name), without a call each."""
+    for t, shape, dtype, what in specs:
+        if t is not None and (t.shape != shape or t.dtype is not dtype):
+            _is(t, shape, dtype, what)
+
+
 def _grouped(a, W_shape, width, offsets, rows, what):
     """(code, G, R, N, K) of a grouped product whose tall operand is a."""
     if a.dim() != 2 or len(W_shape) != 3 or a.shape[1] != width:
@@ -71,16 +78,24 @@ def _grouped(a, W_shape, width, offsets, rows, what):
     return _code(a, what), int(G), int(a.shape[0]), int(N), int(K)
 
 
-def _ws(nbytes, ws, device):
-    return workspace(nbytes, device) if ws is None else ws
+def _workspace(nbytes, like):
+    # new_empty takes half as long as torch.empty with a device
+    return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
 
 
-def _grouped_ws(sizes, ws, device):
-    """(workspace, bytes): the fp32 products do without."""
+_grouped_bytes = 0
+
+
+def _grouped_ws(sizes, ws, like):
+    """(workspace, bytes): the fp32 products do without; one size serves every
+    bf16 product (too small a one would be refused)."""
+    global _grouped_bytes
     if ws is None:
         if sizes[0] == DTYPE_F32:
             return None, 0
-        ws = workspace(lib().moe_grouped_workspace_size(*sizes), device)
+        if not _grouped_bytes:
+            _grouped_bytes = lib().moe_grouped_workspace_size(DTYPE_BF16, 1, 1, 8, 8)
+        ws = _workspace(_grouped_bytes, like)
     return ws, ws.numel()
 
 
@@ -91,9 +106,9 @@ def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
     _is(W, W.shape, x.dtype, "W")
     shape = (x.shape[0], W.shape[1])
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        y = x.new_empty(shape)
     _is(y, shape, x.dtype, "y")
-    ws, nbytes = _grouped_ws(sizes, ws, x.device)
+    ws, nbytes = _grouped_ws(sizes, ws, x)
     check(lib().moe_grouped_matmul(*sizes, *_ptrs(x, W, offsets, rows, y, ws), nbytes,
                                    _stream()), "moe_grouped_matmul")
     return y
@@ -105,9 +120,9 @@ def moe_grouped_matmul_dx(dy, W, offsets, rows=None, dx=None, ws=None):
     _is(W, W.shape, dy.dtype, "W")
     shape = (dy.shape[0], W.shape[2])
     if dx is None:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        dx = dy.new_empty(shape)
     _is(dx, shape, dy.dtype, "dx")
-    ws, nbytes = _grouped_ws(sizes, ws, dy.device)
+    ws, nbytes = _grouped_ws(sizes, ws, dy)
     check(lib().moe_grouped_matmul_dx(*sizes, *_ptrs(dy, W, offsets, rows, dx, ws), nbytes,
                                       _stream()), "moe_grouped_matmul_dx")
     return dx
@@ -126,10 +141,10 @@ def moe_grouped_matmul_dw(dy, x, offsets, rows=None, add=None, dW=None, out_dtyp
     if out_dtype is None:
         out_dtype = next((t.dtype for t in (add, dW) if t is not None), dy.dtype)
     if dW is None:
-        dW = torch.empty(shape, dtype=out_dtype, device=dy.device)
+        dW = dy.new_empty(shape, dtype=out_dtype)
     _is(dW, shape, out_dtype, "dW")
     _is(add, shape, out_dtype, "add")
-    ws, nbytes = _grouped_ws(sizes, ws, dy.device)
+    ws, nbytes = _grouped_ws(sizes, ws, dy)
     check(lib().moe_grouped_matmul_dw(*sizes, *_ptrs(dy, x, offsets, rows), _code(dW, "dW"),
                                       *_ptrs(add, dW, ws), nbytes, _stream()),
           "moe_grouped_matmul_dw")
@@ -143,18 +158,14 @@ def moe_combine_backward(cfg: MoeConfig, dy, Y_perm, gates, topk, pos, keep, off
     T, k, d, dt = cfg.T, cfg.k, cfg.d, _tdtype(cfg)
     R = _rows(cfg)
     if dY_perm is None:
-        dY_perm = torch.empty((R, d), dtype=dt, device=dy.device)
+        dY_perm = dy.new_empty((R, d))
     if dgates is None:
-        dgates = torch.empty_like(gates, dtype=torch.float32)
-    for t, shape, dtype, what in ((dy, (T, d), dt, "dy"), (Y_perm, (R, d), dt, "Y_perm"),
-                                  (dY_perm, (R, d), dt, "dY_perm"),
-                                  (gates, (T, k), torch.float32, "gates"),
-                                  (dgates, (T, k), torch.float32, "dgates"),
-                                  (topk, (T, k), torch.int32, "topk"),
-                                  (pos, (T, k), torch.int32, "pos"),
-                                  (keep, (T, k), torch.uint8, "keep"),
-                                  (offsets, (cfg.E + 1,), torch.int32, "offsets")):
-        _is(t, shape, dtype, what)
+        dgates = torch.empty_like(gates)
+    tk, f32, i32 = (T, k), torch.float32, torch.int32
+    _fit(((dy, (T, d), dt, "dy"), (Y_perm, (R, d), dt, "Y_perm"), (dY_perm, (R, d), dt, "dY_perm"),
+          (gates, tk, f32, "gates"), (dgates, tk, f32, "dgates"), (topk, tk, i32, "topk"),
+          (pos, tk, i32, "pos"), (keep, tk, torch.uint8, "keep"),
+          (offsets, (cfg.E + 1,), i32, "offsets")))
     check(lib().moe_combine_backward(ctypes.byref(cfg), *_ptrs(dy, Y_perm, gates, topk, pos, keep,
                                                                offsets, dY_perm, dgates),
                                      _stream()), "moe_combine_backward")
@@ -187,14 +198,14 @@ def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, 
     counts.  `grads` gives the output buffers (dx_perm alone its own); with
     accumulate the weight gradients are added to what they hold."""
     E, d, F, T, S, Fs = cfg.E, cfg.d, cfg.d_ff, cfg.T, cfg.n_shared, cfg.d_ff_shared
-    dt, dev = _tdtype(cfg), x_perm.device
+    dt = _tdtype(cfg)
     R = _rows(cfg)
     swiglu = cfg.act == 1
     if accumulate and grads is None:
         raise ValueError("accumulate adds to the weight gradients in `grads`")
     if grads is None:
         wt = dt if dw_dtype is None else dw_dtype
-        e = lambda *shape, t=wt: torch.empty(shape, dtype=t, device=dev)
+        e = lambda *shape, t=wt: x_perm.new_empty(shape, dtype=t)
         grads = FFNGrads(dx_perm=e(R, d, t=dt) if dx_perm is None else dx_perm, dW1=e(E, F, d),
                          dW3=e(E, F, d) if swiglu else None, dW2=e(E, d, F))
         if S:
@@ -207,7 +218,7 @@ def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, 
     wt = g.dW1.dtype
     if dw_dtype is not None and dw_dtype != wt:
         raise ValueError(f"dw_dtype {dw_dtype} but dW1 is {wt}")
-    for t, shape, dtype, what in (
+    _fit((
             (x_perm, (R, d), dt, "x_perm"), (dY_perm, (R, d), dt, "dY_perm"),
             (offsets, (E + 1,), torch.int32, "offsets"), (kept, (E,), torch.int32, "kept"),
             (W1, (E, F, d), dt, "W1"), (W3, (E, F, d), dt, "W3"), (W2, (E, d, F), dt, "W2"),
@@ -217,9 +228,9 @@ def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, 
             (g.dW1, (E, F, d), wt, "dW1"), (g.dW3, (E, F, d), wt, "dW3"),
             (g.dW2, (E, d, F), wt, "dW2"), (g.dx_shared, (T, d), dt, "dx_shared"),
             (g.dWs1, (S, Fs, d), wt, "dWs1"), (g.dWs3, (S, Fs, d), wt, "dWs3"),
-            (g.dWs2, (S, d, Fs), wt, "dWs2")):
-        _is(t, shape, dtype, what)
-    ws = _ws(moe_ffn_backward_workspace_size(cfg), ws, dev)
+            (g.dWs2, (S, d, Fs), wt, "dWs2")))
+    if ws is None:
+        ws = _workspace(moe_ffn_backward_workspace_size(cfg), x_perm)
     check(lib().moe_expert_ffn_backward(
         ctypes.byref(cfg), *_ptrs(x_perm, offsets, kept, dY_perm, W1, W3, W2, x, dY_shared, Ws1,
                                   Ws3, Ws2, g.dx_perm, g.dW1, g.dW3, g.dW2, g.dx_shared, g.dWs1,
@@ -242,12 +253,13 @@ def moe_orthogonalize(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), scale=1.0, e
         raise ValueError(f"G is {tuple(G.shape)}: [E, m, n] or [m, n] wanted")
     E, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
     if U is None:
-        U = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+        U = G.new_empty(G.shape, dtype=torch.bfloat16)
     _is(U, G.shape, torch.bfloat16, "U")
     if len(coeffs) != 3:
         raise ValueError(f"coeffs are a, b, c, not {len(coeffs)} numbers")
     c = (ctypes.c_float * 3)(*coeffs)
-    ws = _ws(moe_orthogonalize_workspace_size(E, m, n, steps), ws, G.device)
+    if ws is None:
+        ws = _workspace(moe_orthogonalize_workspace_size(E, m, n, steps), G)
     g, u, w = _ptrs(G, U, ws)
     check(lib().moe_orthogonalize(_code(G, "G"), E, m, n, g, int(steps), c, float(eps),
                                   float(scale), u, w, ws.numel(), _stream()),
