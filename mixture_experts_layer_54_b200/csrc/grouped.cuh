@@ -53,8 +53,9 @@ struct Set {
     int bytes, base_bytes;       // alignment of the rows (32, 16 or 2), found at launch
 };
 
-struct __align__(64) Params {
-    Set set[kSets];
+// A kernel takes as many sets as its launches have: six are 6 KB of arguments.
+template <int SETS>
+struct __align__(64) ParamsOf {
     int nsets, entries;          // set 0 is the ragged one, if any is
     const int32_t *offsets;      // [G + 1]
     const int32_t *rows;         // [G], nullable: offsets[g + 1] - offsets[g]
@@ -69,7 +70,9 @@ struct __align__(64) Params {
     int32_t *status;
     int clear_status;
     unsigned long long timeout_ns;
+    Set set[SETS];
 };
+using Params = ParamsOf<kSets>;
 
 // First row and row count of group g, held inside the buffers whatever the
 // table says.
