@@ -493,7 +493,7 @@ moe_status moe_forward(const moe_config *cfg, const moe_weights *w,
  * serves one call at a time; its contents do not matter, and its first word is
  * the device status word (cleared by the call).  The grouped products in fp32 do
  * without (ws NULL).  Every call is safe to capture in a CUDA graph and gives the
- * same bits on every run. */
+ * same bits on every run.  No output may overlap an input, but where a call says so. */
 
 /* Workspace bytes of the three grouped products; 0 for invalid arguments. */
 size_t moe_grouped_workspace_size(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K);

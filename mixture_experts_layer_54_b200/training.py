@@ -70,12 +70,14 @@ def _fit(specs):
 
 def _grouped(a, W_shape, width, offsets, rows, what):
     """(code, G, R, N, K) of a grouped product whose tall operand is a."""
-    if a.dim() != 2 or len(W_shape) != 3 or a.shape[1] != width:
-        raise ValueError(f"{what} {tuple(a.shape)} does not fit weights {tuple(W_shape)}")
+    shape = a.shape
+    if len(shape) != 2 or len(W_shape) != 3 or shape[1] != width:
+        raise ValueError(f"{what} {tuple(shape)} does not fit weights {tuple(W_shape)}")
     G, N, K = W_shape
     _is(offsets, (G + 1,), torch.int32, "offsets")
-    _is(rows, (G,), torch.int32, "rows")
-    return _code(a, what), int(G), int(a.shape[0]), int(N), int(K)
+    if rows is not None:
+        _is(rows, (G,), torch.int32, "rows")
+    return _code(a, what), G, shape[0], N, K
 
 
 def _workspace(nbytes, like):
@@ -102,12 +104,14 @@ def _grouped_ws(sizes, ws, like):
 def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
     """y[r] = W[g] x[r] for the rows r of each group g: x [R, K], W [G, N, K],
     offsets [G + 1] (and rows [G]) int32.  Rows of no group are not written."""
-    sizes = _grouped(x, W.shape, W.shape[-1], offsets, rows, "x")
-    _is(W, W.shape, x.dtype, "W")
-    shape = (x.shape[0], W.shape[1])
+    W_shape = W.shape
+    sizes = _grouped(x, W_shape, W_shape[-1], offsets, rows, "x")
+    _is(W, W_shape, x.dtype, "W")
+    shape = (sizes[2], sizes[3])
     if y is None:
         y = x.new_empty(shape)
-    _is(y, shape, x.dtype, "y")
+    else:
+        _is(y, shape, x.dtype, "y")
     ws, nbytes = _grouped_ws(sizes, ws, x)
     check(lib().moe_grouped_matmul(*sizes, *_ptrs(x, W, offsets, rows, y, ws), nbytes,
                                    _stream()), "moe_grouped_matmul")
@@ -116,12 +120,14 @@ def moe_grouped_matmul(x, W, offsets, rows=None, y=None, ws=None):
 
 def moe_grouped_matmul_dx(dy, W, offsets, rows=None, dx=None, ws=None):
     """Gradient of moe_grouped_matmul by x: dx[r] = W[g]^T dy[r], dy [R, N]."""
-    sizes = _grouped(dy, W.shape, W.shape[-2], offsets, rows, "dy")
-    _is(W, W.shape, dy.dtype, "W")
-    shape = (dy.shape[0], W.shape[2])
+    W_shape = W.shape
+    sizes = _grouped(dy, W_shape, W_shape[-2], offsets, rows, "dy")
+    _is(W, W_shape, dy.dtype, "W")
+    shape = (sizes[2], sizes[4])
     if dx is None:
         dx = dy.new_empty(shape)
-    _is(dx, shape, dy.dtype, "dx")
+    else:
+        _is(dx, shape, dy.dtype, "dx")
     ws, nbytes = _grouped_ws(sizes, ws, dy)
     check(lib().moe_grouped_matmul_dx(*sizes, *_ptrs(dy, W, offsets, rows, dx, ws), nbytes,
                                       _stream()), "moe_grouped_matmul_dx")
@@ -137,12 +143,13 @@ def moe_grouped_matmul_dw(dy, x, offsets, rows=None, add=None, dW=None, out_dtyp
         raise ValueError("dy and x are [R, N] and [R, K]")
     shape = (G, dy.shape[1], x.shape[1])
     sizes = _grouped(dy, shape, shape[1], offsets, rows, "dy")
-    _is(x, (dy.shape[0], shape[2]), dy.dtype, "x")
+    _is(x, (sizes[2], shape[2]), dy.dtype, "x")
     if out_dtype is None:
         out_dtype = next((t.dtype for t in (add, dW) if t is not None), dy.dtype)
     if dW is None:
         dW = dy.new_empty(shape, dtype=out_dtype)
-    _is(dW, shape, out_dtype, "dW")
+    else:
+        _is(dW, shape, out_dtype, "dW")
     _is(add, shape, out_dtype, "add")
     ws, nbytes = _grouped_ws(sizes, ws, dy)
     check(lib().moe_grouped_matmul_dw(*sizes, *_ptrs(dy, x, offsets, rows), _code(dW, "dW"),
@@ -157,15 +164,15 @@ def moe_combine_backward(cfg: MoeConfig, dy, Y_perm, gates, topk, pos, keep, off
     not written."""
     T, k, d, dt = cfg.T, cfg.k, cfg.d, _tdtype(cfg)
     R = _rows(cfg)
-    if dY_perm is None:
-        dY_perm = dy.new_empty((R, d))
-    if dgates is None:
-        dgates = torch.empty_like(gates)
-    tk, f32, i32 = (T, k), torch.float32, torch.int32
-    _fit(((dy, (T, d), dt, "dy"), (Y_perm, (R, d), dt, "Y_perm"), (dY_perm, (R, d), dt, "dY_perm"),
+    rd, tk, f32, i32 = (R, d), (T, k), torch.float32, torch.int32
+    _fit(((dy, (T, d), dt, "dy"), (Y_perm, rd, dt, "Y_perm"), (dY_perm, rd, dt, "dY_perm"),
           (gates, tk, f32, "gates"), (dgates, tk, f32, "dgates"), (topk, tk, i32, "topk"),
           (pos, tk, i32, "pos"), (keep, tk, torch.uint8, "keep"),
           (offsets, (cfg.E + 1,), i32, "offsets")))
+    if dY_perm is None:
+        dY_perm = dy.new_empty(rd)
+    if dgates is None:
+        dgates = torch.empty_like(gates)
     check(lib().moe_combine_backward(ctypes.byref(cfg), *_ptrs(dy, Y_perm, gates, topk, pos, keep,
                                                                offsets, dY_perm, dgates),
                                      _stream()), "moe_combine_backward")
