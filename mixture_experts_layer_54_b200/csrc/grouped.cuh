@@ -62,7 +62,8 @@ struct __align__(64) ParamsOf {
     int n_rows;                  // rows of the tall buffers; the table is held inside them
     int fp16;                    // operands are fp16 (else bf16)
     // scratch of tiles cut along their contraction: parts' accumulators, and a
-    // counter for each warp of each cut tile (any contents).  NULL: no tile is cut
+    // counter for each warp of each cut tile (any contents, but a captured launch's
+    // counters are cleared first: clear_for_replay).  NULL: no tile is cut
     float *partial;
     unsigned long long *counters;
     int partial_bytes;
@@ -98,6 +99,16 @@ enum Layout { A_K_B_K = 0, A_K_B_MN = 1, A_MN_B_MN = 2 };
 enum Tiles { PAIR_256, ONE_128, ONE_32 };
 
 cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s);
+
+// The counters of cut tiles go by the tag of their launch, a new one for every call
+// of launch_tc.  A captured launch keeps its tag, so what a replay that gave up left
+// in the counters would count as the next replay's: while the stream is being
+// captured this clears them, once before the launches of a call (0.5 to 1.7 us of a
+// replay; nothing otherwise).
+cudaError_t clear_for_replay(unsigned long long *counters, cudaStream_t s);
+// Whether tiles of this contraction may be cut at all: four blocks at least
+// (split_plan).
+inline bool may_cut(int64_t contraction) { return contraction > 3 * 128; }
 
 // Maps of a [groups, rows, cols] 2-byte tensor with row pitch ld (group_stride in
 // elements) for the operand's role: K-major (cols is the contraction), boxes of

@@ -581,7 +581,7 @@ __device__ __forceinline__ void store_odd(uint8_t *stg, int lane, const uint32_t
 // This warp's part of a cut tile is written; true for the last of the parts,
 // which then sees them all.  The counter's upper 48 bits are the launch's tag:
 // any other tag there (what the memory held before) counts as zero, so nothing
-// has to be cleared first.
+// has to be cleared first, but before a replay (clear_for_replay).
 __device__ __forceinline__ bool last_part(unsigned long long *count, unsigned long long tag,
                                           int parts, int lane)
 {
@@ -1367,6 +1367,13 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     }
 }
 
+__global__ void __launch_bounds__(1024) clear_counters_kernel(unsigned long long *counters)
+{
+    pdl_wait();
+    pdl_trigger();
+    counters[blockIdx.x * 1024 + threadIdx.x] = 0;
+}
+
 template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI, int SETS, int AR = 128>
 cudaError_t launch_sets(const Params &all, cudaStream_t s)
 {
@@ -1472,6 +1479,17 @@ int b_box(Epi epi, Tiles tiles)   // SwiGLU: a box of W1 and one of W3
 int dh_box(Tiles tiles) { return tiles == PAIR_256 ? kBnAct / 2 : kBnAct; }
 
 int stage_k(Epi epi, Tiles tiles) { return epi == EPI_SWIGLU && tiles != PAIR_256 ? 64 : 128; }
+
+cudaError_t clear_for_replay(unsigned long long *counters, cudaStream_t s)
+{
+    static_assert(kCounterBytes % (8 * 1024) == 0, "counters");
+    cudaStreamCaptureStatus capture;
+    const cudaError_t err = cudaStreamIsCapturing(s, &capture);
+    if (err != cudaSuccess || capture == cudaStreamCaptureStatusNone)
+        return err;
+    return launch_pdl(clear_counters_kernel, dim3(kCounterBytes / (8 * 1024)), dim3(1024), 0, s,
+                      counters);
+}
 
 cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s)
 {

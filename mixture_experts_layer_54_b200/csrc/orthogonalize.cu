@@ -304,7 +304,9 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     cblocks = cblocks > most ? most : cblocks;
     // X0 needs its low half unless G is bf16 (exact in one term) or this is the only step
     const bool lo0 = !bf16 && steps > 1;
-    cudaError_t err;
+    cudaError_t err = clear_for_replay(w.counters, s);
+    if (err != cudaSuccess)
+        return err;
     if (bf16) {
         const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(G);
         err = launch_pdl(square_sums_kernel<__nv_bfloat16>, dim3(parts, E), dim3(256), 0, s, g, mn,

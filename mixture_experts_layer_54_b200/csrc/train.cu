@@ -110,6 +110,11 @@ cudaError_t rows_tc(const Table &t, int G, int64_t R, int N, int K, const void *
     if (!ok)
         return cudaErrorInvalidValue;
     set_cut(p, status);
+    if (may_cut(a.K)) {
+        const cudaError_t e = clear_for_replay(p.counters, s);
+        if (e != cudaSuccess)
+            return e;
+    }
     return launch_tc(p, EPI_ROWS, back ? A_K_B_MN : A_K_B_K, tiles, s);
 }
 
@@ -343,6 +348,9 @@ cudaError_t ffn_grad_tc(const moe_config &c, const Table &t, const FfnArgs &a, c
     }
     if (!ok)
         return cudaErrorInvalidValue;
+    set_cut(p, status);   // not for these tiles, which are whole, but for the calls' below
+    if ((e = clear_for_replay(p.counters, s)) != cudaSuccess)
+        return e;
     if ((e = launch_tc(p, epi, A_K_B_K, hid, s)) != cudaSuccess)
         return e;
 
@@ -531,6 +539,11 @@ moe_status moe_grouped_matmul_dw(int32_t dtype, int32_t G, int64_t R, int32_t N,
                 dw_dtype == MOE_DTYPE_F32, tiles))
         return MOE_ERR_CUDA;
     set_cut(p, ws);
+    if (may_cut(R)) {
+        const cudaError_t e = clear_for_replay(p.counters, s);
+        if (e != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
     return cuda_status(launch_tc(p, EPI_DW, A_MN_B_MN, tiles, s));
 }
 

@@ -1,0 +1,88 @@
+"""Edges of the training calls: what an earlier launch left in a workspace, sums
+over very long contractions, updates far below eps, and the promised accuracy."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_54_b200 as moe
+from test_gpu_training import BF, F32, F64, QUINTIC, ffn_case, newton_schulz, randn, table, within
+
+pytestmark = pytest.mark.gpu
+
+
+class KernelNode(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("shared", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+TAG_AT = 56   # of ParamsOf in csrc/grouped.cuh: the launch's tag in the counters
+
+
+def launch_tags(graph):
+    """Tags of the grouped kernels of a captured graph, from their arguments."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    g, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert cu.cuGraphGetNodes(g, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(g, nodes, ctypes.byref(n)) == 0
+    tags = []
+    for node in nodes:
+        kind = ctypes.c_int()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value != 0:   # a kernel
+            continue
+        p = KernelNode()
+        assert cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        if p.block[0] in (320, 352):   # ten or eleven warps: the grouped kernel
+            first = ctypes.c_void_p.from_address(p.params).value
+            tags.append(ctypes.c_uint64.from_address(first + TAG_AT).value)
+    return tags
+
+
+def capture(call):
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        out = call()
+    tags = launch_tags(g)
+    g.instantiate()
+    return g, out, tags
+
+
+@pytest.mark.parametrize("kind", ["y", "dx", "dw", "few"])
+def test_counters_left_by_a_launch_that_gave_up(kind):
+    """A replayed launch has the tag of the replay before.  Counters as one leaves
+    them whose parts did not all arrive must not count as this launch's own."""
+    sizes, N, K = {"y": ([600], 256, 4096), "dx": ([600], 4096, 256), "dw": ([9000], 128, 128),
+                   "few": ([5, 40], 136, 8192)}[kind]
+    off, _, R, spans = table(sizes, False)
+    G = len(sizes)
+    x, dy = randn(R, K, seed=1), randn(R, N, seed=2)
+    W = randn(G, N, K, seed=3, scale=K ** -0.5)
+    ws = moe.workspace(moe.lib().moe_grouped_workspace_size(1, G, R, N, K), "cuda")
+    out = {"y": torch.zeros_like(dy), "few": torch.zeros_like(dy), "dx": torch.zeros_like(x),
+           "dw": torch.zeros((G, N, K), dtype=F32, device="cuda")}[kind]
+    call = {"y": lambda: moe.moe_grouped_matmul(x, W, off, y=out, ws=ws),
+            "dx": lambda: moe.moe_grouped_matmul_dx(dy, W, off, dx=out, ws=ws),
+            "dw": lambda: moe.moe_grouped_matmul_dw(dy, x, off, dW=out, ws=ws)}
+    call = call["y" if kind == "few" else kind]
+    graph, _, tags = capture(call)
+    assert len(tags) == 1 and tags[0] != 0
+    counters = ws[256:256 + (16 << 10)].view(torch.int64)
+    for seed, arrived in enumerate((1, 2, 3, 4, 6, 9, 15), 4):
+        x.copy_(randn(R, K, seed=seed))
+        dy.copy_(randn(R, N, seed=seed + 20))
+        out.zero_()
+        call()
+        want = out.clone()
+        out.zero_()
+        left = tags[0] << 16 | arrived
+        counters.fill_(left - (1 << 64) if left >> 63 else left)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert moe.moe_device_status(ws) == 0
+        assert torch.equal(out, want)
