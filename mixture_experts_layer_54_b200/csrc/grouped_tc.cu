@@ -599,7 +599,10 @@ __device__ __forceinline__ bool last_part(unsigned long long *count, unsigned lo
             seen = now;
         }
     }
+    // lane 0 saw the other parts arrive; a shuffle alone orders no memory, so the
+    // other lanes' reads of those parts wait for lane 0 here
     last = __shfl_sync(0xffffffffu, last, 0);
+    __syncwarp();
     __threadfence();
     return last;
 }
