@@ -578,6 +578,30 @@ __device__ __forceinline__ void store_odd(uint8_t *stg, int lane, const uint32_t
                 stg + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
 }
 
+// The loading warp has issued `n` stages.  Bounded by the time from one stage to the
+// next: the tails may lie any number of tiles apart, so a limit on the whole wait
+// would give up on a launch longer than that with nothing wrong.
+__device__ __forceinline__ bool wait_loaded(const volatile int *loaded, int n, const Ctl &c)
+{
+    int seen = *loaded;
+    uint64_t t0 = global_ns();
+    while (seen < n) {
+        __nanosleep(64);
+        const int now = *loaded;
+        if (now != seen) {
+            seen = now;
+            t0 = global_ns();
+        } else if (*c.abort) {
+            return false;
+        } else if (global_ns() - t0 > c.timeout_ns) {
+            *c.abort = 1;
+            atomicExch(c.status, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
 // This warp's part of a cut tile is written; true for the last of the parts,
 // which then sees them all.  The counter's upper 48 bits are the launch's tag:
 // any other tag there (what the memory held before) counts as zero, so nothing
@@ -684,6 +708,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_BAR + 8 * (3 * STAGES + 5));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *loaded = abort_flag + 1;   // EPI_DW: stages issued, for the tails' warp
     int2 *span = reinterpret_cast<int2 *>(smem + S::OFF_TAB);   // [groups] first row, rows
     int *tstart = reinterpret_cast<int *>(span + kMaxE);        // [entries + 1]
     int *plan_slot = tstart + kEntries + 1;                     // the Plan
@@ -706,6 +731,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
+        *loaded = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -802,7 +828,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
 
     if (warp == 0) {
         // ================= loads (both CTAs) =================
-        int stage = 0;
+        int stage = 0, stages = 0;
         uint32_t phase = 0;
         int issued = 0;
         uint32_t last_phase = 0;   // bit s: phase of stage s's last use
@@ -890,6 +916,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             }
                         }
                     }
+                    if (EPI == EPI_DW && lane == 0)
+                        *loaded = ++stages;
                     if (!ahead && tile + units < total)
                         next = decode<BM, BN, S::BK>(p, tstart, span, pl, tile + units);
                     ahead = true;
@@ -1040,7 +1068,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                 !ragged_tail<S::BK>(rem))
                 continue;
             const int stage = (blocks - 1) % STAGES;
-            ok = wait_bar(tail_bar(stage), parity >> stage & 1, ctl);
+            ok = lane > 0 || wait_loaded(loaded, blocks, ctl);
+            ok = __all_sync(0xffffffffu, ok) && wait_bar(tail_bar(stage), parity >> stage & 1, ctl);
             ok = __all_sync(0xffffffffu, ok);
             parity ^= 1u << stage;
             // 128 bytes a row, so 8 lanes a row: four rows of a box at a time

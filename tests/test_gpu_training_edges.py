@@ -86,3 +86,22 @@ def test_counters_left_by_a_launch_that_gave_up(kind):
         torch.cuda.synchronize()
         assert moe.moe_device_status(ws) == 0
         assert torch.equal(out, want)
+
+
+def test_a_tail_behind_seconds_of_work():
+    """About three seconds of whole tiles, then one group that ends inside a step of
+    16 rows: the wait for its tail is not longer than a stage.  (The even groups all
+    have the same rows, or so much work would not fit in memory.)"""
+    R, N, K, G = 7 << 17, 8192, 2048, 255
+    x = torch.empty((R, K), dtype=BF, device="cuda").bernoulli_(0.5)
+    dy = torch.empty((R, N), dtype=BF, device="cuda").bernoulli_(0.5)
+    off = torch.zeros(G + 1, dtype=torch.int32)
+    off[1::2] = R
+    rows = torch.full((G,), R, dtype=torch.int32)
+    rows[-1] = 7
+    ws = moe.workspace(moe.lib().moe_grouped_workspace_size(1, G, R, N, K), "cuda")
+    dW = moe.moe_grouped_matmul_dw(dy, x, off.cuda(), rows.cuda(), ws=ws)
+    assert moe.moe_device_status(ws) == 0
+    assert torch.equal(dW[-1].float(), dy[:7].float().T @ x[:7].float())   # whole numbers up to 7
+    for g in range(1, G - 1):
+        assert torch.equal(dW[g], dW[0]) if g % 2 == 0 else not dW[g].any()
