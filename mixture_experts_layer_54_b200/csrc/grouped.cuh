@@ -49,6 +49,7 @@ struct Set {
     int64_t base_group;
     float alpha, beta;
     const float *scale;          // nullable: alpha / scale[g]^scale_pow, beta / scale[g]
+    const float *scale_to;       // nullable: alpha and beta times scale_to[g]
     int scale_pow;
     int bytes, base_bytes;       // alignment of the rows (32, 16 or 2), found at launch
 };

@@ -1108,6 +1108,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
             // base is read a chunk ahead: the first before the products are done
             uint32_t base[EPI == EPI_NS ? 16 : 1];
             const bool based = EPI == EPI_NS && s.base && lane < rv;
+            float alpha = s.alpha, beta = s.beta;
             const uint8_t *from = reinterpret_cast<const uint8_t *>(
                 static_cast<const __half *>(s.base) + (int64_t)t.g * s.base_group +
                 (int64_t)(m + lane) * s.base_ld + t.n0);
@@ -1126,6 +1127,11 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                 const int c = half * (BN / 2);
                 if (based && c < c_end)
                     load_row<2>(from + 2 * c, 2 * (s.N - t.n0 - c), s.base_bytes, base);
+                if (s.scale) {
+                    const float sc = s.scale[t.g], to = s.scale_to ? s.scale_to[t.g] : 1.f;
+                    alpha = s.scale_pow == 2 ? alpha / sc / sc : alpha * to / sc;
+                    beta = beta * to / sc;
+                }
             }
             if (!wait_bar(tfull_bar(slot), (it >> 1) & 1, ctl))
                 break;
@@ -1316,12 +1322,6 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
                         store_traded(w, static_cast<uint16_t *>(s.out) + at, s.ld, lane, rv, cv);
                     } else if constexpr (EPI == EPI_NS) {
-                        float alpha = s.alpha, beta = s.beta;
-                        if (s.scale) {
-                            const float sc = s.scale[t.g];
-                            alpha = s.scale_pow == 2 ? alpha / sc / sc : alpha / sc;
-                            beta /= sc;
-                        }
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] *= alpha;

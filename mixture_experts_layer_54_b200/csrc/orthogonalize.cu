@@ -4,9 +4,9 @@
 // which drives the singular values towards 1 and keeps the singular vectors.
 //
 // Bound by the tensor cores.  The products run on the fp16 pipe (the rate of
-// bf16, 3 more bits) on fp16 copies of X, A and B = b A + c A A with fixed
-// powers of two as scales, so nothing is near the ends of fp16's range while
-// the singular values stay below about 2.8.  A step multiplies small singular
+// bf16, 3 more bits) on fp16 copies of X, A and B = b A + c A A with powers of
+// two as scales (orthogonalize.cuh), so nothing is near the ends of fp16's range
+// while the singular values stay below about 2.8.  A step multiplies small singular
 // values by a = 3.4, so what a rounding of X (2^-11) leaves among them in the
 // first of five steps comes out 140 times as large: 2e-2 of the result for an
 // update of rank 32, measured.  That noise only passes through a X, since B
@@ -18,9 +18,11 @@
 // with the product, as a on B's diagonal (one array less to read in its
 // epilogue: 8 to 6 bytes an element), and the last step reads hi alone: near
 // singular value 1 the same X in both places is the more exact.  A bf16 G times
-// a power of two is exact in one term.  A and B are symmetric: only tiles on or
-// below the diagonal are computed and mirrored.
+// a power of two is exact in one term (but for elements below 2^-30 of its norm).
+// A and B are symmetric: only tiles on or below the diagonal are computed and
+// mirrored.
 #include "grouped.cuh"
+#include "orthogonalize.cuh"
 
 #include <cuda_fp16.h>
 #include <math.h>
@@ -31,8 +33,6 @@ namespace grp {
 
 namespace {
 
-// stored value = true value times these
-constexpr float kSX = 8192.f, kSA = 8192.f, kSB = 2048.f;
 constexpr int kMaxParts = 256;
 
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
@@ -134,13 +134,18 @@ __global__ void __launch_bounds__(256)
         out[e * kMaxParts + blockIdx.x] = v;
 }
 
-// X = G 2^k as one or two fp16 terms, 2^k the power of two that brings |G| + eps
-// into (kSX / 2, kSX]; scale[e] = 2^k (|G| + eps) is then what X stands over.
+struct Coeffs {
+    float a, b, c;
+};
+
+// X = G 2^k as one or two fp16 terms, 2^k the power of two that brings |G| into
+// (kSX / 2, kSX]; scale[e] = 2^k (|G| + eps) is then what X stands over.  scale[i E
+// + e], from i = 1 on, is X's factor before step i.
 // Rows of a multiple of 8 elements are one run of them; others go row by row.
 template <typename T>
 __global__ void __launch_bounds__(256)
     scale_kernel(const T *G, int m, int n, int64_t ld, int parts, bool vec, const double *sums,
-                 float eps, __half *hi, __half *lo, float *scale)
+                 float eps, Coeffs co, int steps, __half *hi, __half *lo, float *scale)
 {
     pdl_wait();
     pdl_trigger();
@@ -154,11 +159,12 @@ __global__ void __launch_bounds__(256)
         for (int s = 16; s; s >>= 1)
             v += __shfl_xor_sync(0xffffffffu, v, s);
         if (threadIdx.x == 0) {
-            const double norm = sqrt(v) + (double)eps;
+            const double size = sqrt(v), norm = size + (double)eps;
             double sc = norm;   // zero with eps = 0: 0 / 0 as the formula has it
             int k = 0;
             if (isfinite(norm) && norm > 0) {
-                k = 13 - (int)ceil(log2(norm));
+                k = 13 - (int)ceil(log2(size > 0 ? size : norm));
+                k = min(k, 100 - (int)ceil(log2(norm)));   // sc stays in fp32's range
                 sc = exp2((double)k) * norm;
             } else if (!isfinite(norm)) {
                 sc = nan("");   // an infinity or NaN in G: the whole update is NaN
@@ -166,8 +172,14 @@ __global__ void __launch_bounds__(256)
             const int k0 = min(max(k, -126), 126);
             s_mul[0] = (float)exp2((double)k0);
             s_mul[1] = (float)exp2((double)(k - k0));
-            if (blockIdx.x == 0)
+            if (blockIdx.x == 0) {
                 scale[e] = (float)sc;
+                float u = norm > 0 ? (float)(size / norm) : 0.f;
+                for (int i = 1; i < steps; ++i) {
+                    u = next_bound(u, co.a, co.b, co.c);
+                    scale[(int64_t)i * gridDim.y + e] = kSX * power2(x_shift(u));
+                }
+            }
         }
     }
     __syncthreads();
@@ -256,7 +268,7 @@ Bufs carve(int64_t E, int64_t m, int64_t n, int steps, void *ws)
     b.counters = static_cast<unsigned long long *>(take(kCounterBytes));
     b.partial = static_cast<float *>(take(kPartialBytes));
     b.sums = static_cast<double *>(take((size_t)E * kMaxParts * 8));
-    b.scale = static_cast<float *>(take((size_t)E * 4));
+    b.scale = static_cast<float *>(take((size_t)steps * E * 4));
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 2; ++j)
             b.X[i][j] = static_cast<__half *>(take(steps > 1 || i + j == 0 ? x : 0));
@@ -304,6 +316,7 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     cblocks = cblocks > most ? most : cblocks;
     // X0 needs its low half unless G is bf16 (exact in one term) or this is the only step
     const bool lo0 = !bf16 && steps > 1;
+    const Coeffs co{a, b, c};
     cudaError_t err = clear_for_replay(w.counters, s);
     if (err != cudaSuccess)
         return err;
@@ -313,16 +326,16 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
                          parts, vsum, w.sums);
         if (err == cudaSuccess)
             err = launch_pdl(scale_kernel<__nv_bfloat16>, dim3((unsigned)cblocks, E), dim3(256), 0,
-                             s, g, m, n, ldx, parts, vrow, (const double *)w.sums, eps, w.X[0][0],
-                             lo0 ? w.X[0][1] : nullptr, w.scale);
+                             s, g, m, n, ldx, parts, vrow, (const double *)w.sums, eps, co, steps,
+                             w.X[0][0], lo0 ? w.X[0][1] : nullptr, w.scale);
     } else {
         const float *g = static_cast<const float *>(G);
         err = launch_pdl(square_sums_kernel<float>, dim3(parts, E), dim3(256), 0, s, g, mn, parts,
                          vsum, w.sums);
         if (err == cudaSuccess)
             err = launch_pdl(scale_kernel<float>, dim3((unsigned)cblocks, E), dim3(256), 0, s, g, m,
-                             n, ldx, parts, vrow, (const double *)w.sums, eps, w.X[0][0],
-                             lo0 ? w.X[0][1] : nullptr, w.scale);
+                             n, ldx, parts, vrow, (const double *)w.sums, eps, co, steps,
+                             w.X[0][0], lo0 ? w.X[0][1] : nullptr, w.scale);
     }
     if (err != cudaSuccess)
         return err;
@@ -363,8 +376,9 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
         t.out = w.A;
         t.ld = (int)lda;
         t.out_group = p * lda;
-        t.alpha = i == 0 ? kSA : kSA / (kSX * kSX);
-        t.scale = i == 0 ? w.scale : nullptr;
+        const float *scale_i = w.scale + (int64_t)i * E;
+        t.alpha = kSA;
+        t.scale = scale_i;
         t.scale_pow = 2;
         if (!ok)
             return cudaErrorInvalidValue;
@@ -405,10 +419,10 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
             ok &= map_k(&t.a[0], X, m, n, ldx, E, m * ldx, 128, sk, nw);
             ok &= map_k(&t.b[0], w.B, p, p, lda, E, p * lda, box, sk, pw);
         }
-        const float mult = last ? scale : kSX;
-        t.alpha = i == 0 ? mult / kSB : mult / (kSB * kSX);
-        t.beta = i == 0 ? a * mult : a * mult / kSX;
-        t.scale = i == 0 ? w.scale : nullptr;
+        t.alpha = (last ? scale : 1.f) / kSB;
+        t.beta = a;   // with lo, which the last step does without
+        t.scale = scale_i;
+        t.scale_to = last ? nullptr : scale_i + E;
         t.scale_pow = 1;
         t.base = Xlo;
         t.base_ld = (int)ldx;

@@ -13,6 +13,7 @@
 //   A = X X^T;  B = a I + b A + c A A;  X = B X.
 // A and B share one buffer of 128 x 128 in two terms.
 #include "grouped.cuh"
+#include "orthogonalize.cuh"
 
 #include <cuda_fp16.h>
 #include <math.h>
@@ -24,7 +25,6 @@ using namespace tc;
 
 namespace {
 
-constexpr float kSX = 8192.f, kSA = 8192.f, kSB = 2048.f;   // stored over true values
 constexpr int BLOCK = 128 * 128;                            // bytes of 64 columns of one term
 constexpr int THREADS = 256;
 
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double part[THREADS / 32];
-    __shared__ float s_mul, s_over;
+    __shared__ float s_mul, s_over, s_size;
     __shared__ int again;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar = smem_u32(&bar_mem);
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     if (blockIdx.x == 0 && tid == 0)
         *s.status = 0;
 
-    // |G| and X = G / (|G| + eps), times kSX
+    // |G| and X = G / (|G| + eps), times its factor
     const T *G = static_cast<const T *>(s.G) + (int64_t)blockIdx.x * mn;
     float acc[4] = {};
     for (int i = tid; i < mn; i += 4 * THREADS) {
@@ -201,16 +201,19 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
             v = block_sum();
     }
     if (tid == 0) {
-        const double norm = sqrt(v) + (double)s.eps;
+        const double size = sqrt(v), norm = size + (double)s.eps;
         // G times a power of two near kSX / |G| (exact), then the rest of the factor
         double mul = 1.0;
         if (isfinite(norm) && norm > 0)
-            mul = exp2((double)min(max(13 - (int)ceil(log2(norm)), -126), 126));
+            mul = exp2((double)min(max(13 - (int)ceil(log2(size > 0 ? size : norm)), -126), 126));
         s_mul = (float)mul;
-        s_over = (float)(isfinite(norm) ? (double)kSX / (mul * norm) : nan(""));
+        s_size = norm > 0 ? (float)(size / norm) : 0.f;
+        s_over = (float)(isfinite(norm) ? (double)kSX * power2(x_shift(s_size)) / (mul * norm) : nan(""));
     }
     __syncthreads();
     const float mul = s_mul, over = s_over;
+    float bound = s_size;         // of X's singular values
+    int shift = x_shift(bound);   // X's factor is kSX times this power of two
     for (int i = tid; i < mn; i += THREADS) {
         const int r = i / s.n, c = i - r * s.n;
         const uint32_t o = wide ? place(r, c) : place(c, r);
@@ -260,18 +263,22 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
 
     for (int i = 0; ok && i < s.steps; ++i) {
         const bool last = i + 1 == s.steps;
+        const int was = shift;
+        bound = next_bound(bound, s.a, s.b, s.c);
+        shift = x_shift(bound);
         written();
         if (tid == 0)
             square(t_s, ax, qk);
         if (!(ok = done()))
             break;
+        const float fa = kSA / (kSX * kSX) * power2(-was) * power2(-was);
         if (rows)
             for (int c = 16 * half; c < 16 * pk; c += 32) {
                 float f[16];
                 tmem_ld16(t_s + lanes + c, f);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    f[j] *= kSA / (kSX * kSX);
+                    f[j] *= fa;
                 put16(sh, sl, row, c, f);
             }
         written();
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
         if (!(ok = done()))
             break;
         if (rows) {
-            const float f0 = (last ? s.scale / kSX : 1.f) / kSB;
+            const float f0 = (last ? s.scale / kSX : power2(shift)) / kSB * power2(-was);
             for (int c = 16 * half; c < 16 * qk; c += 32) {
                 float f[16];
                 tmem_ld16(t_x + lanes + c, f);

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_54_b200 as moe
-from test_gpu_training import BF, F32, F64, QUINTIC, ffn_case, newton_schulz, randn, table, within
+from test_gpu_training import BF, F32, F64, NS_TOL, QUINTIC, ffn_case, newton_schulz, randn, table, within
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,26 @@ def test_a_tail_behind_seconds_of_work():
     assert torch.equal(dW[-1].float(), dy[:7].float().T @ x[:7].float())   # whole numbers up to 7
     for g in range(1, G - 1):
         assert torch.equal(dW[g], dW[0]) if g % 2 == 0 else not dW[g].any()
+
+
+# the promised error of five steps, and one rounding to bf16
+PROMISED = 2e-3 + 2.0 ** -8
+CUBIC = (1.5, -0.5, 0.0)
+
+
+@pytest.mark.parametrize("m,n", [(48, 80), (90, 40), (300, 700), (520, 264)])
+@pytest.mark.parametrize("steps,coeffs,tol", [(1, QUINTIC, PROMISED), (2, QUINTIC, PROMISED),
+                                              (5, QUINTIC, PROMISED), (30, CUBIC, NS_TOL)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_orthogonalize_far_below_eps(m, n, steps, coeffs, tol, dtype):
+    """|G| from eps down to 1e-24 eps: the result is a to the number of steps times
+    |G| / eps, small but not nothing, until the steps have brought it near 1."""
+    eps = 1e-7
+    G = torch.stack([randn(m, n, seed=i, dtype=F32) for i in range(7)])
+    sizes = torch.tensor([1.0, 1e-3, 1e-6, 1e-9, 1e-12, 1e-18, 1e-24], device="cuda")
+    G = (G / G.flatten(1).norm(dim=1)[:, None, None] * (eps * sizes)[:, None, None]).to(dtype)
+    U = moe.moe_orthogonalize(G, steps=steps, coeffs=coeffs, eps=eps)
+    ref = newton_schulz(G, steps, coeffs, eps)
+    for e in range(len(sizes)):
+        rel = ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item()
+        assert rel <= tol, (e, rel)
