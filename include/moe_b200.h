@@ -585,9 +585,10 @@ size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t
  * towards 1: X = G[e] / (|G[e]|_F + eps), then `steps` times A = X X^T and
  * X = a X + (b A + c A A) X (X^T X from the right when m > n), U[e] = scale X.
  *   G [E, m, n] fp32 or bf16 (`dtype`), any alignment of its elements; U
- *   [E, m, n] bf16.  coeffs (host): a, b, c; they must keep the singular values
- *   below 2.8 and those of b A + c A A below 16, as 3.4445, -4.775, 2.0315 or
- *   1.5, -0.5, 0 do (fp16 intermediates).  1 <= E <= 1024, m, n <= 2^20, 1 <=
+ *   [E, m, n] bf16.  coeffs (host): a, b, c.  From singular values between 0 and 1
+ *   the steps before the last must keep them below 2.8, and every step |a + b s + c
+ *   s^2| below 31 for their squares s (fp16 intermediates; else MOE_ERR_SHAPE): 3.4445,
+ *   -4.775, 2.0315 and 1.5, -0.5, 0 do.  1 <= E <= 1024, m, n <= 2^20, 1 <=
  *   steps <= 32.  A matrix of zeros gives zeros (NaN when eps is 0); one with an
  *   infinity or NaN gives NaN, in its own update only.
  * The products take fp16 operands (X itself is held as two fp16 terms): the

@@ -263,6 +263,37 @@ moe_status rows_call(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K, 
     return cuda_status(launch_simt(p, s));
 }
 
+// Whether every X, X X^T and a I + b A + c A A of `steps` steps stays inside fp16 as
+// they are stored (times 8192, 8192 and 2048), for singular values from 0 to 1 at
+// the start: p(x) = x g(x^2), g(s) = a + b s + c s^2, at the ends of the interval and
+// where p' or g' is zero.
+bool steps_in_range(double a, double b, double c, int steps)
+{
+    double u = 1;
+    for (int i = 0; i < steps; ++i) {
+        if (!(u <= 2.8))   // 8192 u^2 <= 64225
+            return false;
+        double top = 0, most = fabs(a);
+        auto look = [&](double s) {
+            if (!(s >= 0 && s <= u * u))
+                return;
+            const double g = fabs(a + s * (b + s * c));
+            most = g > most ? g : most;
+            top = sqrt(s) * g > top ? sqrt(s) * g : top;
+        };
+        look(u * u);
+        look(-b / (2 * c));
+        const double q = sqrt(9 * b * b - 20 * a * c);   // p' = a + 3 b s + 5 c s^2
+        look((-3 * b + q) / (10 * c));
+        look((-3 * b - q) / (10 * c));
+        look(-a / (3 * b));                              // c = 0
+        if (!(most <= 31))   // 2048 g <= 63488
+            return false;
+        u = top;
+    }
+    return true;
+}
+
 // Scratch of the FFN backward: hidden activations and their gradients, and in
 // fp32 also u, v and dh (in bf16 those never leave the accumulators).
 struct FfnScratch {
@@ -643,6 +674,8 @@ moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, con
     const moe_status st = check_ws(ws, ws_bytes, need);
     if (st != MOE_OK)
         return st;
+    if (!steps_in_range(coeffs[0], coeffs[1], coeffs[2], steps))
+        return MOE_ERR_SHAPE;
     return cuda_status(launch_orthogonalize(dtype == MOE_DTYPE_BF16, E, m, n, G, steps, coeffs[0],
                                             coeffs[1], coeffs[2], eps, scale, U, ws,
                                             reinterpret_cast<cudaStream_t>(stream)));

@@ -128,3 +128,18 @@ def test_orthogonalize_far_below_eps(m, n, steps, coeffs, tol, dtype):
     for e in range(len(sizes)):
         rel = ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item()
         assert rel <= tol, (e, rel)
+
+
+@pytest.mark.parametrize("coeffs,steps,last", [((2.79, 0.0, 0.0), 2, 2.79 ** 2), ((1.0, 29.5, 0.0), 1, 30.5),
+                                               ((0.0, 0.0, 1.3), 2, 1.3 ** 6), ((-30.9, 0.0, 0.0), 1, -30.9)])
+@pytest.mark.parametrize("m,n", [(40, 64), (300, 264)])
+def test_orthogonalize_at_the_edge_of_its_range(coeffs, steps, last, m, n):
+    """Coefficients just inside what is refused, on a matrix of one singular value,
+    which the norm makes 1: nothing overflows.  (X, B and the product: each operand
+    is off by at most 2^-11, five times over for the fifth power.)"""
+    u, v = randn(2, m, 1, seed=1, dtype=F32), randn(2, 1, n, seed=2, dtype=F32)
+    G = u @ v
+    U = moe.moe_orthogonalize(G, steps=steps, coeffs=coeffs, eps=0.0)
+    ref = last * G.to(F64) / torch.linalg.matrix_norm(G.to(F64))[:, None, None]
+    for e in range(2):
+        assert ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item() <= 2.0 ** -8 + 20 * 2.0 ** -11

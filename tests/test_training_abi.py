@@ -159,3 +159,17 @@ def test_binding_refuses_wrong_shapes_types_and_places():
 
 def test_package_exports_every_training_binding():
     assert set(training.__all__) <= set(moe.__all__)
+
+
+@pytest.mark.parametrize("coeffs,steps", [
+    ((2.85, 0.0, 0.0), 2), ((2.7, 0.0, 0.0), 3), ((1.0, 31.0, 0.0), 1), ((32.0, -31.5, 0.0), 1),
+    ((-33.0, 0.0, 0.0), 1), ((3.0, -4.0, 2.0), 5), ((0.0, 0.0, 3.0), 2), ((0.5, 40.0, -40.0), 2),
+    ((1e30, 1.0, 1e-30), 2), ((1.0, -3e38, 3e38), 1)])
+def test_orthogonalize_refuses_steps_that_leave_fp16(coeffs, steps):
+    """(E, m, n) of the form of many launches and of the one-launch form."""
+    if torch.cuda.is_available():
+        pytest.skip("pointers of no memory: without a device nothing can be launched with them")
+    for m, n in ((160, 240), (16, 16)):
+        c = (ctypes.c_float * 3)(*coeffs)
+        status = moe.lib().moe_orthogonalize(BF16, 2, m, n, P, steps, c, 1e-7, 1.0, P, P, 1 << 30, None)
+        assert status == _abi.MOE_ERR_SHAPE
