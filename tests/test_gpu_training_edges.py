@@ -143,3 +143,46 @@ def test_orthogonalize_at_the_edge_of_its_range(coeffs, steps, last, m, n):
     ref = last * G.to(F64) / torch.linalg.matrix_norm(G.to(F64))[:, None, None]
     for e in range(2):
         assert ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item() <= 2.0 ** -8 + 20 * 2.0 ** -11
+
+
+def update(kind, E, m, n, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m * n)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    if kind == "noise":
+        G = r(E, m, n)
+    elif kind == "rank_32":
+        G = r(E, m, 32) @ r(E, 32, n)
+    else:   # singular values 1, 1/2, 1/3, ...
+        p = min(m, n)
+        u, v = torch.linalg.qr(r(E, m, p))[0], torch.linalg.qr(r(E, n, p))[0]
+        G = (u / torch.arange(1, p + 1, device="cuda")) @ v.mT
+    return (1e-3 * G).to(dtype)
+
+
+@pytest.mark.parametrize("kind", ["noise", "rank_32", "decaying"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n", [(300, 700), (520, 264), (1024, 512), (130, 2100), (2000, 160)])
+def test_orthogonalize_keeps_its_promise(m, n, dtype, kind):
+    """2e-3 in 2-norm, and the rounding to bf16: at most half a step, evenly spread,
+    so 2^-8 / sqrt(3) of the norm."""
+    G = update(kind, 2, m, n, dtype)
+    U, ref = moe.moe_orthogonalize(G), newton_schulz(G, 5, QUINTIC)
+    for e in range(2):
+        rel = ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item()
+        assert rel <= 2e-3 + 2.0 ** -8 / math.sqrt(3), (e, rel)
+
+
+@pytest.mark.parametrize("kind", ["noise", "rank_32", "decaying"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n", [(128, 320), (48, 80), (320, 128), (34, 33)])
+def test_orthogonalize_of_small_matrices_is_as_in_fp32(m, n, dtype, kind):
+    """Terms of 22 bits: 2e-2 for 11 bits in the worst kind, so 1e-5 for 22.  What an
+    element is off by beyond half a bf16 step is at most twice its error before the
+    rounding (twice, where the step doubles)."""
+    G = update(kind, 2, m, n, dtype)
+    U, ref = moe.moe_orthogonalize(G).to(F64), newton_schulz(G, 5, QUINTIC)
+    half = torch.ldexp(torch.ones_like(ref), torch.frexp(ref)[1] - 9)
+    for e in range(2):
+        over = ((U[e] - ref[e]).abs() - half[e]).clamp(min=0).norm() / ref[e].norm()
+        assert over.item() <= 2e-5, (e, over.item())
