@@ -88,8 +88,8 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, const int32_t
 
 // Epilogues: EPI_ROWS bf16 rows; EPI_DW fp32 or bf16 with an addend; EPI_NS
 // the Newton-Schulz stores; EPI_GELU / EPI_SWIGLU the hidden activations and
-// their gradients.
-enum Epi { EPI_ROWS = 0, EPI_DW = 1, EPI_NS = 2, EPI_GELU = 3, EPI_SWIGLU = 4 };
+// their gradients.  EPI_ROWS_LONG is launch_tc's own choice for EPI_ROWS.
+enum Epi { EPI_ROWS = 0, EPI_DW = 1, EPI_NS = 2, EPI_GELU = 3, EPI_SWIGLU = 4, EPI_ROWS_LONG = 5 };
 
 // Operand layouts: MN = the contraction index is the row index of the stored
 // matrix (its other index is contiguous), K = the contraction is contiguous.

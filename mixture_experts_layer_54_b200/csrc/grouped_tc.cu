@@ -27,6 +27,10 @@
 // where fp32 rounding alone leaves 3e-7), so a weight gradient over many rows
 // is summed in accumulators of 512 rows each, which the epilogue adds up in
 // registers (round to nearest) while the next one fills: 128 values a thread.
+// Products and input gradients, which end in bf16, take accumulators of 4096 (5e-6;
+// a single one left 2e-5 at 14336 and 1e-3 at 2^20), in kernels of their own: with
+// the sums' registers the short contractions took 2 to 5% longer.  u, v and dh (over
+// the layer's width) and the stacks keep a single one.
 //
 // Work is dealt as tiles, one to each CTA (pair) in turn.  Where the last round
 // would leave most of them idle (or, with few rows, every round), the tiles of
@@ -65,6 +69,7 @@ constexpr int EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int STG_WARP = 32 * 64;        // staging tile of an epilogue warp: 32 rows of 64 bytes
 constexpr int RING_BYTES = 192 * 1024;
+constexpr int kLongRows = 4096;          // EPI_ROWS_LONG: contraction in one accumulator
 
 // AR: rows of A a CTA takes, 128, or 32 for groups of few rows: the MMA's other
 // rows read on into the next bytes of the ring, their results are never stored,
@@ -72,6 +77,7 @@ constexpr int RING_BYTES = 192 * 1024;
 template <int CTAS, int BN, int EPI, int AR>
 struct Shape {
     static constexpr bool ACT = EPI == EPI_GELU || EPI == EPI_SWIGLU;
+    static constexpr bool ROWS = EPI == EPI_ROWS || EPI == EPI_ROWS_LONG;
     static constexpr int BM = AR * CTAS;
     static constexpr int A_BYTES = AR * 128;             // AR rows x 64 elements
     static constexpr int FIRST_EPI = EPI == EPI_DW ? 3 : 2;   // first of the epilogue warps
@@ -96,9 +102,10 @@ struct Shape {
     static constexpr int OFF_BAR = OFF_STG + (STAGED ? EPI_WARPS * STG_WARP : 0);
     static constexpr int OFF_TAB = OFF_BAR + 256;
     static constexpr int SMEM = OFF_TAB + 8 * kMaxE + 4 * (kEntries + 4) + 1024;   // + alignment slack
-    // EPI_DW: contraction rows summed in one accumulator before the epilogue
-    // adds it, in registers, to the tile's running sum (0: all of them)
-    static constexpr int CHUNK = EPI == EPI_DW ? 512 : 0;
+    // contraction summed in one accumulator before the epilogue adds it, in
+    // registers, to the tile's running sum (0: all of it)
+    static constexpr int CHUNK = EPI == EPI_DW ? 512 : EPI == EPI_ROWS_LONG ? kLongRows : 0;
+    static constexpr int CHUNK_BLOCKS = CHUNK > 0 ? CHUNK / BK : 1;
     // TMEM columns.  Plain: two accumulators of BN.  GELU: u and dh, twice.
     // SwiGLU: u | v once (256 columns), dh twice behind it.
     static constexpr int DH_COL = EPI == EPI_SWIGLU ? 2 * BN : BN;
@@ -854,7 +861,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                 const int b_row = t.n0 + (uv && CTAS == 2 ? 0 : (int)rank * (BN / CTAS));
                 // a tile of few rows loads no more than 32 (the MMA's other rows are
                 // whatever the stage holds; they are never stored)
-                const bool few = EPI == EPI_ROWS && s.has_few && t.mg - t.m0 <= 32;
+                const bool few = S::ROWS && s.has_few && t.mg - t.m0 <= 32;
                 const int a_rows = few ? 32 : AR;
                 const CUtensorMap *am = few ? &s.a_few : &s.a[ph];
                 const CUtensorMap *bm = uv && rank == 1 ? &s.b3 : &s.b[bi];
@@ -988,7 +995,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                                            ((uint32_t)((uv ? 2 * BN : BN) >> 3) << 17);
                     const int end = min(t.kbs, t.b1 - sg * t.kbs);
                     for (; kb < end; ++kb, ++n) {
-                        if (S::CHUNK > 0 && n > 0 && n % (S::CHUNK > 0 ? S::CHUNK / S::BK : 1) == 0) {
+                        if (S::CHUNK > 0 && n > 0 && n % S::CHUNK_BLOCKS == 0) {
                             // this accumulator is full: on to the other one
                             commit_all<CTAS>(tfull_bar(slot));
                             ++it;
@@ -1150,7 +1157,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             ((int64_t)t.cut * t.parts + t.part) * part_step +
                             (int64_t)wid * (BN / 8) * 32;
             unsigned long long *count = p.counters + t.cut * (CTAS * S::ROW_WARPS) + wid;
-            if constexpr (EPI == EPI_DW) {
+            if (EPI == EPI_DW || (S::CHUNK > 0 && t.b1 - t.b0 > S::CHUNK_BLOCKS)) {
                 float sum[BN / 2];
                 if (t.b0 == t.b1) {   // nothing was accumulated: an empty group's sum
 #pragma unroll
@@ -1162,7 +1169,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                         tmem_ld32(tq + slot * BN + half * (BN / 2) + 32 * i, sum + 32 * i);
                 }
                 bool ok = true;
-                for (int k = S::CHUNK / S::BK; k < t.b1 - t.b0; k += S::CHUNK / S::BK) {
+                for (int k = S::CHUNK_BLOCKS; k < t.b1 - t.b0; k += S::CHUNK_BLOCKS) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -1212,9 +1219,23 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                     for (int i = 0; i < BN / 2; i += 32)
                         add_parts(from + 8 * i, part_step, t.parts, sum + i);
                 }
-                if (rv > 0)
-                    store_sums<BN / 2>(s, sum, at0 + half * (BN / 2), lane,
-                                       rv, c_end - half * (BN / 2), bytes);
+                if constexpr (EPI == EPI_DW) {
+                    if (rv > 0)
+                        store_sums<BN / 2>(s, sum, at0 + half * (BN / 2), lane,
+                                           rv, c_end - half * (BN / 2), bytes);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < BN / 64; ++i) {
+                        const int c = half * (BN / 2) + 32 * i;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = pack_bf16(sum[32 * i + 2 * j], sum[32 * i + 2 * j + 1]);
+                        if (c < c_end)
+                            store_traded(w, static_cast<uint16_t *>(s.out) + at0 + c, s.ld, lane, rv,
+                                         s.N - t.n0 - c);
+                    }
+                }
                 continue;
             }
             bool released = false;
@@ -1316,7 +1337,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                     } else {
                         tmem_ld32(tq + slot * BN + c, v);
                     }
-                    if constexpr (EPI == EPI_ROWS) {
+                    if constexpr (S::ROWS) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
@@ -1455,13 +1476,28 @@ cudaError_t launch_sets(const Params &all, cudaStream_t s)
 template <int CTAS, int BN, bool A_MN, bool B_MN, int EPI, int AR = 128>
 cudaError_t launch_one(const Params &p, cudaStream_t s)
 {
+    constexpr bool rows = EPI == EPI_ROWS || EPI == EPI_ROWS_LONG;
     constexpr int most = EPI == EPI_DW ? kSets
-                         : EPI == EPI_NS || (EPI == EPI_ROWS && (!B_MN || AR < 128)) ? 1 : 2;
+                         : EPI == EPI_NS || (rows && (!B_MN || AR < 128)) ? 1 : 2;
     if (p.nsets > most)
         return cudaErrorInvalidValue;
     if (most > 1 && !(EPI == EPI_GELU || EPI == EPI_SWIGLU) && p.nsets == 1)
         return launch_sets<CTAS, BN, A_MN, B_MN, EPI, 1, AR>(p, s);
     return launch_sets<CTAS, BN, A_MN, B_MN, EPI, most, AR>(p, s);
+}
+
+template <int EPI>
+cudaError_t launch_rows(const Params &p, Layout layout, Tiles tiles, cudaStream_t s)
+{
+    const bool pair = tiles == PAIR_256;
+    if (tiles == ONE_32)
+        return layout == A_K_B_MN ? launch_one<1, 128, false, true, EPI, 32>(p, s)
+                                  : launch_one<1, 128, false, false, EPI, 32>(p, s);
+    if (layout == A_K_B_MN)
+        return pair ? launch_one<2, 256, false, true, EPI>(p, s)
+                    : launch_one<1, 128, false, true, EPI>(p, s);
+    return pair ? launch_one<2, 256, false, false, EPI>(p, s)
+                : launch_one<1, 128, false, false, EPI>(p, s);
 }
 
 constexpr int kBnAct = 128;
@@ -1526,8 +1562,11 @@ cudaError_t clear_for_replay(unsigned long long *counters, cudaStream_t s)
 cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream_t s)
 {
     int ents = 0;
+    int64_t longest = 0;   // contraction
     for (int i = 0; i < p.nsets; ++i) {
         Set &v = p.set[i];
+        if ((int64_t)v.segs * v.K > longest)
+            longest = (int64_t)v.segs * v.K;
         v.ent0 = ents;
         // what every row of every output (and addend) is aligned to
         const int64_t esz = epi == EPI_DW && v.out_f32 ? 4 : 2;
@@ -1562,14 +1601,9 @@ cudaError_t launch_tc(Params &p, Epi epi, Layout layout, Tiles tiles, cudaStream
         return pair ? launch_one<2, 256, true, true, EPI_DW>(p, s)
                     : launch_one<1, 128, true, true, EPI_DW>(p, s);
     case EPI_ROWS:
-        if (tiles == ONE_32)
-            return layout == A_K_B_MN ? launch_one<1, 128, false, true, EPI_ROWS, 32>(p, s)
-                                      : launch_one<1, 128, false, false, EPI_ROWS, 32>(p, s);
-        if (layout == A_K_B_MN)
-            return pair ? launch_one<2, 256, false, true, EPI_ROWS>(p, s)
-                        : launch_one<1, 128, false, true, EPI_ROWS>(p, s);
-        return pair ? launch_one<2, 256, false, false, EPI_ROWS>(p, s)
-                    : launch_one<1, 128, false, false, EPI_ROWS>(p, s);
+    case EPI_ROWS_LONG:
+        return longest > kLongRows ? launch_rows<EPI_ROWS_LONG>(p, layout, tiles, s)
+                                   : launch_rows<EPI_ROWS>(p, layout, tiles, s);
     case EPI_NS:
         if (layout == A_K_B_MN)
             return pair ? launch_one<2, 256, false, true, EPI_NS>(p, s)

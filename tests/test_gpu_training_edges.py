@@ -107,6 +107,30 @@ def test_a_tail_behind_seconds_of_work():
         assert torch.equal(dW[g], dW[0]) if g % 2 == 0 else not dW[g].any()
 
 
+def half_step(ref):
+    """Half a bf16 step at every element."""
+    return torch.ldexp(torch.ones_like(ref), torch.frexp(ref)[1] - 9)
+
+
+@pytest.mark.parametrize("R,N,K,G", [(60, 264, 1 << 17, 1), (5, 136, 1 << 20, 1), (200, 128, 1 << 18, 2),
+                                     (600, 4000, 1 << 15, 1), (1600, 1288, 14336, 8)])
+def test_products_over_long_contractions(R, N, K, G):
+    """Sums of values of one sign, where every truncation counts: 4096 of them in one
+    accumulator (256 steps of 16, each truncated), up to 256 of those added up and
+    16 parts of a tile, all relative to the sum."""
+    off, _, rows, spans = table([R // G] * G, False)
+    x = randn(rows, K, seed=1).abs()
+    W = randn(G, N, K, seed=3, scale=K ** -0.5).abs()
+    Wt = W.mT.contiguous()
+    y = moe.moe_grouped_matmul(x, W, off)
+    dx = moe.moe_grouped_matmul_dx(x, Wt, off)   # [G, K, N]: the same sums, W read across its rows
+    tol = (256 + math.ceil(K / 4096) + 16) * 2.0 ** -23
+    for g, (lo, hi) in enumerate(spans):
+        ref = x[lo:hi].to(F64) @ W[g].to(F64).T
+        for got in (y, dx):
+            within(got[lo:hi], ref, half_step(ref) + tol * ref)
+
+
 # the promised error of five steps, and one rounding to bf16
 PROMISED = 2e-3 + 2.0 ** -8
 CUBIC = (1.5, -0.5, 0.0)
@@ -182,7 +206,7 @@ def test_orthogonalize_of_small_matrices_is_as_in_fp32(m, n, dtype, kind):
     rounding (twice, where the step doubles)."""
     G = update(kind, 2, m, n, dtype)
     U, ref = moe.moe_orthogonalize(G).to(F64), newton_schulz(G, 5, QUINTIC)
-    half = torch.ldexp(torch.ones_like(ref), torch.frexp(ref)[1] - 9)
+    half = half_step(ref)
     for e in range(2):
         over = ((U[e] - ref[e]).abs() - half[e]).clamp(min=0).norm() / ref[e].norm()
         assert over.item() <= 2e-5, (e, over.item())
