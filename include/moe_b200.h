@@ -602,12 +602,29 @@ moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, con
                              void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * moe_training_status - whether a bounded wait of any training call has run out on
+ * the current device since the last clear (MOE_OK or MOE_ERR_DEVICE_TIMEOUT; that
+ * call's results are not valid).  Unlike the status word of one call's workspace it
+ * stays when the workspace is gone or the next call clears it.  *status is host
+ * memory; `stream` is synchronised, and the calls of other streams count as far as
+ * they are done.
+ */
+moe_status moe_training_status(int32_t *status, moe_stream_t stream);
+
+/* Clear it (asynchronous, on `stream`). */
+moe_status moe_clear_training_status(moe_stream_t stream);
+
+/* moe_probe_wait_timeout for moe_training_status, without a workspace. */
+moe_status moe_probe_training_timeout(uint64_t timeout_ns, moe_stream_t stream);
+
+/*
  * moe_device_status - read the device status word that the bounded waits of
  * the tensor-core kernels (router, expert GEMMs) set when they give up
- * (MOE_OK or MOE_ERR_DEVICE_TIMEOUT).  moe_route and moe_expert_ffn clear it
- * when they start, moe_forward once for the whole layer.  ws is the workspace
- * passed to those calls; *status is host memory.  Synchronises `stream` (a cudaMemcpyAsync followed by a stream
- * synchronise) - the only call in this library that does.
+ * (MOE_OK or MOE_ERR_DEVICE_TIMEOUT).  moe_route, moe_expert_ffn and the training
+ * calls clear it when they start, moe_forward once for the whole layer.  ws is the
+ * workspace passed to those calls; *status is host memory.  Synchronises `stream` (a
+ * cudaMemcpyAsync followed by a stream synchronise): in this library only this call
+ * and moe_training_status do.
  */
 moe_status moe_device_status(const void *ws, int32_t *status,
                              moe_stream_t stream);

@@ -17,7 +17,8 @@ from .ops import (CapacityOut, HostStream, MoEForward, moe_bias_update, moe_capa
                   moe_stage_workspace_size, moe_validate, moe_workspace_size, weights_struct,
                   StagedForward,
                   workspace)
-from .training import (FFNGrads, moe_combine_backward, moe_expert_ffn_backward,
+from .training import (FFNGrads, moe_clear_training_status, moe_combine_backward,
+                       moe_expert_ffn_backward, moe_probe_training_timeout, moe_training_status,
                        moe_ffn_backward_workspace_size, moe_grouped_matmul, moe_grouped_matmul_dw,
                        moe_grouped_matmul_dx, moe_orthogonalize, moe_orthogonalize_workspace_size)
 
@@ -33,4 +34,5 @@ __all__ = ["MOE_ROW_ALIGN", "CapacityFactorError", "MoEError", "MoeConfig", "Moe
            "workspace", "StagedForward", "FFNGrads", "moe_combine_backward",
            "moe_expert_ffn_backward", "moe_ffn_backward_workspace_size", "moe_grouped_matmul",
            "moe_grouped_matmul_dw", "moe_grouped_matmul_dx", "moe_orthogonalize",
-           "moe_orthogonalize_workspace_size"]
+           "moe_orthogonalize_workspace_size", "moe_training_status", "moe_clear_training_status",
+           "moe_probe_training_timeout"]

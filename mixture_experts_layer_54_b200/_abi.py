@@ -90,6 +90,9 @@ SIGNATURES = {
     "moe_orthogonalize": (ctypes.c_int, [ctypes.c_int32] * 4 +
                           [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_float), ctypes.c_float,
                            ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "moe_training_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int32), _P]),
+    "moe_clear_training_status": (ctypes.c_int, [_P]),
+    "moe_probe_training_timeout": (ctypes.c_int, [ctypes.c_uint64, _P]),
     "moe_device_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
     "moe_clear_device_status": (ctypes.c_int, [_P, _P]),
     "moe_probe_wait_timeout": (ctypes.c_int, [_P, ctypes.c_uint64, _P]),

@@ -65,6 +65,8 @@ using namespace tc;
 
 namespace {
 
+__device__ int32_t g_gave_up;   // MOE_ERR_DEVICE_TIMEOUT after any call here gave up
+
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int STG_WARP = 32 * 64;        // staging tile of an epilogue warp: 32 rows of 64 bytes
@@ -601,8 +603,7 @@ __device__ __forceinline__ bool wait_loaded(const volatile int *loaded, int n, c
         } else if (*c.abort) {
             return false;
         } else if (global_ns() - t0 > c.timeout_ns) {
-            *c.abort = 1;
-            atomicExch(c.status, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
+            give_up(c);
             return false;
         }
     }
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
     const bool leader = rank == 0;
     const int unit = blockIdx.x / CTAS, units = gridDim.x / CTAS;
-    const Ctl ctl{abort_flag, p.status, p.timeout_ns};
+    const Ctl ctl{abort_flag, p.status, p.timeout_ns, &g_gave_up};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -1420,6 +1421,18 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     }
 }
 
+// One bounded wait on a barrier that nothing arrives on (diagnostic).
+__global__ void probe_kernel(unsigned long long timeout_ns)
+{
+    __shared__ uint64_t bar;
+    __shared__ int abort_flag;
+    mbar_init(smem_u32(&bar), 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    const Ctl ctl{&abort_flag, &g_gave_up, timeout_ns, nullptr};
+    wait_bar(smem_u32(&bar), 0, ctl);
+}
+
 __global__ void __launch_bounds__(1024) clear_counters_kernel(unsigned long long *counters)
 {
     pdl_wait();
@@ -1547,6 +1560,17 @@ int b_box(Epi epi, Tiles tiles)   // SwiGLU: a box of W1 and one of W3
 int dh_box(Tiles tiles) { return tiles == PAIR_256 ? kBnAct / 2 : kBnAct; }
 
 int stage_k(Epi epi, Tiles tiles) { return epi == EPI_SWIGLU && tiles != PAIR_256 ? 64 : 128; }
+
+cudaError_t gave_up_grouped(int32_t **word)
+{
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_gave_up);
+}
+
+cudaError_t launch_grouped_probe(unsigned long long timeout_ns, cudaStream_t s)
+{
+    probe_kernel<<<1, 1, 0, s>>>(timeout_ns);
+    return cudaGetLastError();
+}
 
 cudaError_t clear_for_replay(unsigned long long *counters, cudaStream_t s)
 {

@@ -25,6 +25,8 @@ using namespace tc;
 
 namespace {
 
+__device__ int32_t g_gave_up;   // MOE_ERR_DEVICE_TIMEOUT after any call here gave up
+
 constexpr int BLOCK = 128 * 128;                            // bytes of 64 columns of one term
 constexpr int THREADS = 256;
 
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     __shared__ int again;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar = smem_u32(&bar_mem);
-    const Ctl ctl{&abort_flag, s.status, 2000000000ull};
+    const Ctl ctl{&abort_flag, s.status, 2000000000ull, &g_gave_up};
     if (tid == 0) {
         mbar_init(bar, 1);
         abort_flag = 0;
@@ -360,6 +362,11 @@ int small_smem(int m, int n)
 }
 
 }  // namespace
+
+cudaError_t gave_up_small(int32_t **word)
+{
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_gave_up);
+}
 
 // X in two terms, A in two: what fits in a block's shared memory, and 128 rows
 bool orthogonalize_is_small(int m, int n)

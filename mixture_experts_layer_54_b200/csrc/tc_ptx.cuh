@@ -67,7 +67,17 @@ struct Ctl {
     volatile int *abort;
     int32_t *status;
     uint64_t timeout_ns;
+    int32_t *gave_up;   // nullable: a word that outlives the workspace with the status
 };
+
+// A bounded wait ran out: all roles of the CTA leave, and the host can read it.
+__device__ __forceinline__ void give_up(const Ctl &c)
+{
+    *c.abort = 1;
+    atomicExch(c.status, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
+    if (c.gave_up)
+        atomicExch(c.gave_up, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
+}
 
 // Wait for the phase of `bar` with the given parity to complete.  Gives up
 // (returns false) when the time limit passed or, if honor_abort, when another
@@ -87,8 +97,7 @@ __device__ __noinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctl &
             if (honor_abort && *c.abort)
                 return false;
             if (global_ns() - t0 > c.timeout_ns) {
-                *c.abort = 1;
-                atomicExch(c.status, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
+                give_up(c);
                 return false;
             }
         }

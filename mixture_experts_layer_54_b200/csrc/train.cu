@@ -18,6 +18,10 @@ size_t orthogonalize_bytes(int64_t E, int64_t m, int64_t n, int steps);
 cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, int steps, float a,
                                  float b, float c, float eps, float scale, void *U, void *ws,
                                  cudaStream_t s);
+// The words that say that a bounded wait ran out on this device.
+cudaError_t gave_up_grouped(int32_t **word);
+cudaError_t gave_up_small(int32_t **word);
+cudaError_t launch_grouped_probe(unsigned long long timeout_ns, cudaStream_t s);
 }  // namespace grp
 
 using namespace grp;
@@ -644,6 +648,41 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
         return cuda_status(ffn_grad_tc(c, t, a, f, dw_dtype == MOE_DTYPE_F32, accumulate != 0, ws,
                                        s));
     return cuda_status(ffn_grad_simt(c, t, a, f, accumulate != 0, ws, s));
+}
+
+moe_status moe_training_status(int32_t *status, moe_stream_t stream)
+{
+    if (!status)
+        return MOE_ERR_NULL;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int32_t *word[2], seen[2] = {0, 0};
+    if (gave_up_grouped(&word[0]) != cudaSuccess || gave_up_small(&word[1]) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    for (int i = 0; i < 2; ++i)
+        if (cudaMemcpyAsync(&seen[i], word[i], 4, cudaMemcpyDeviceToHost, s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    *status = seen[0] ? seen[0] : seen[1];
+    return MOE_OK;
+}
+
+moe_status moe_clear_training_status(moe_stream_t stream)
+{
+    int32_t *word[2];
+    if (gave_up_grouped(&word[0]) != cudaSuccess || gave_up_small(&word[1]) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    for (int i = 0; i < 2; ++i)
+        if (clear_word(word[i], reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    return MOE_OK;
+}
+
+moe_status moe_probe_training_timeout(uint64_t timeout_ns, moe_stream_t stream)
+{
+    if (timeout_ns > 2000000000ull)
+        return MOE_ERR_SHAPE;
+    return cuda_status(launch_grouped_probe(timeout_ns, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t steps)

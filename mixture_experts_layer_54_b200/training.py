@@ -274,6 +274,26 @@ def moe_orthogonalize(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), scale=1.0, e
     return U
 
 
+def moe_training_status() -> int:
+    """0, or MOE_ERR_DEVICE_TIMEOUT when a bounded wait of any training call has run
+    out on the current device since the last clear (also of calls that made their
+    own workspace).  Synchronises the current stream."""
+    st = ctypes.c_int32()
+    check(lib().moe_training_status(ctypes.byref(st), _stream()), "moe_training_status")
+    return int(st.value)
+
+
+def moe_clear_training_status():
+    check(lib().moe_clear_training_status(_stream()), "moe_clear_training_status")
+
+
+def moe_probe_training_timeout(timeout_ns: int):
+    """Diagnostic: one bounded wait that must run out and set the status."""
+    check(lib().moe_probe_training_timeout(int(timeout_ns), _stream()),
+          "moe_probe_training_timeout")
+
+
 __all__ = ["moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
            "moe_combine_backward", "moe_expert_ffn_backward", "moe_ffn_backward_workspace_size",
-           "FFNGrads", "moe_orthogonalize", "moe_orthogonalize_workspace_size"]
+           "FFNGrads", "moe_orthogonalize", "moe_orthogonalize_workspace_size", "moe_training_status",
+           "moe_clear_training_status", "moe_probe_training_timeout"]

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_54_b200 as moe
+from mixture_experts_layer_54_b200 import _abi
 from test_gpu_training import BF, F32, F64, NS_TOL, QUINTIC, ffn_case, newton_schulz, randn, table, within
 
 pytestmark = pytest.mark.gpu
@@ -210,3 +211,20 @@ def test_orthogonalize_of_small_matrices_is_as_in_fp32(m, n, dtype, kind):
     for e in range(2):
         over = ((U[e] - ref[e]).abs() - half[e]).clamp(min=0).norm() / ref[e].norm()
         assert over.item() <= 2e-5, (e, over.item())
+
+
+def test_a_wait_that_ran_out_is_not_lost_with_its_workspace():
+    """A bounded wait of the training kernels, given 50 ms on a barrier that nothing
+    arrives on: the status stays through later calls that make their own workspace,
+    until it is cleared, and the calls go on."""
+    assert moe.moe_training_status() == 0
+    moe.moe_probe_training_timeout(50_000_000)
+    off, _, R, spans = table([60, 40], False)
+    x, W = randn(R, 64, seed=1), randn(2, 72, 64, seed=2, scale=1 / 8)
+    G = randn(2, 48, 40, seed=3)
+    y, U = moe.moe_grouped_matmul(x, W, off), moe.moe_orthogonalize(G)
+    assert moe.moe_training_status() == _abi.MOE_ERR_DEVICE_TIMEOUT
+    moe.moe_clear_training_status()
+    assert torch.equal(moe.moe_grouped_matmul(x, W, off)[3:103], y[3:103])
+    assert torch.equal(moe.moe_orthogonalize(G), U)
+    assert moe.moe_training_status() == 0

@@ -173,3 +173,8 @@ def test_orthogonalize_refuses_steps_that_leave_fp16(coeffs, steps):
         c = (ctypes.c_float * 3)(*coeffs)
         status = moe.lib().moe_orthogonalize(BF16, 2, m, n, P, steps, c, 1e-7, 1.0, P, P, 1 << 30, None)
         assert status == _abi.MOE_ERR_SHAPE
+
+
+def test_training_status_checks_its_arguments():
+    assert moe.lib().moe_training_status(None, None) == _abi.MOE_ERR_NULL
+    assert moe.lib().moe_probe_training_timeout(2_000_000_001, None) == _abi.MOE_ERR_SHAPE
