@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(THREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1)
     int *mtiles = tstart + (kMaxE + 1);                         // [E]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Ctl ctl{abort_flag, p.status, p.timeout_ns, nullptr};
+    const Ctl ctl{abort_flag, p.status, p.timeout_ns};
 
     // ---- set-up: barriers, TMEM, tile table ----
     if (threadIdx.x == 0) {
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(THREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1)
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-    const Ctl ctl{abort_flag, p.status, p.timeout_ns, nullptr};
+    const Ctl ctl{abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES2; ++s) {
@@ -1115,7 +1115,7 @@ __global__ void wait_probe_kernel(int32_t *status, unsigned long long timeout_ns
     mbar_init(b, 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    const Ctl ctl{&abort_flag, status, timeout_ns, nullptr};
+    const Ctl ctl{&abort_flag, status, timeout_ns};
     wait_bar(b, 0, ctl);
 }
 

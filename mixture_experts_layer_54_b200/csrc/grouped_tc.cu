@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
     const bool leader = rank == 0;
     const int unit = blockIdx.x / CTAS, units = gridDim.x / CTAS;
-    const Ctl ctl{abort_flag, p.status, p.timeout_ns, &g_gave_up};
+    const Ctl ctl{abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -1408,6 +1408,8 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
     __syncthreads();
     if (CTAS == 2)
         cluster_sync();
+    if (threadIdx.x == 0 && *abort_flag)
+        atomicExch(&g_gave_up, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         if (CTAS == 2)
@@ -1429,7 +1431,7 @@ __global__ void probe_kernel(unsigned long long timeout_ns)
     mbar_init(smem_u32(&bar), 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    const Ctl ctl{&abort_flag, &g_gave_up, timeout_ns, nullptr};
+    const Ctl ctl{&abort_flag, &g_gave_up, timeout_ns};
     wait_bar(smem_u32(&bar), 0, ctl);
 }
 

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     __shared__ int again;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar = smem_u32(&bar_mem);
-    const Ctl ctl{&abort_flag, s.status, 2000000000ull, &g_gave_up};
+    const Ctl ctl{&abort_flag, s.status, 2000000000ull};
     if (tid == 0) {
         mbar_init(bar, 1);
         abort_flag = 0;
@@ -346,6 +346,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && abort_flag)
+        atomicExch(&g_gave_up, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)

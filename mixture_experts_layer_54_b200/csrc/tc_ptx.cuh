@@ -67,7 +67,6 @@ struct Ctl {
     volatile int *abort;
     int32_t *status;
     uint64_t timeout_ns;
-    int32_t *gave_up;   // nullable: a word that outlives the workspace with the status
 };
 
 // A bounded wait ran out: all roles of the CTA leave, and the host can read it.
@@ -75,8 +74,6 @@ __device__ __forceinline__ void give_up(const Ctl &c)
 {
     *c.abort = 1;
     atomicExch(c.status, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
-    if (c.gave_up)
-        atomicExch(c.gave_up, (int32_t)MOE_ERR_DEVICE_TIMEOUT);
 }
 
 // Wait for the phase of `bar` with the given parity to complete.  Gives up
