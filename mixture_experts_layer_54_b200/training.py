@@ -6,7 +6,7 @@ buffers that are not given are allocated with torch.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -220,7 +220,7 @@ def moe_expert_ffn_backward(cfg: MoeConfig, x_perm, offsets, kept, dY_perm, W1, 
             grads.dWs1, grads.dWs2 = e(S, Fs, d), e(S, d, Fs)
             grads.dWs3 = e(S, Fs, d) if swiglu else None
     elif dx_perm is not None:
-        grads.dx_perm = dx_perm
+        grads = replace(grads, dx_perm=dx_perm)   # the caller's stays as it is
     g = grads
     wt = g.dW1.dtype
     if dw_dtype is not None and dw_dtype != wt:

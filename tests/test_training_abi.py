@@ -178,3 +178,17 @@ def test_orthogonalize_refuses_steps_that_leave_fp16(coeffs, steps):
 def test_training_status_checks_its_arguments():
     assert moe.lib().moe_training_status(None, None) == _abi.MOE_ERR_NULL
     assert moe.lib().moe_probe_training_timeout(2_000_000_001, None) == _abi.MOE_ERR_SHAPE
+
+
+def test_ffn_backward_leaves_the_callers_gradients_alone():
+    """dx_perm beside `grads` is used for this call; the caller's object keeps its own."""
+    cfg = moe.moe_config(T=4, d=64, E=2, k=1, d_ff=64, act=0, dtype=1, cf=1.0)
+    R, bf = moe.moe_perm_rows(cfg), torch.bfloat16
+    x, W = torch.zeros((R, 64), dtype=bf), torch.zeros((2, 64, 64), dtype=bf)
+    off, kept = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    mine = torch.zeros((R, 64), dtype=bf)
+    grads = moe.FFNGrads(dx_perm=mine, dW1=W, dW3=None, dW2=W)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_expert_ffn_backward(cfg, x, off, kept, x, W, None, W, grads=grads,
+                                    dx_perm=torch.zeros_like(x), ws=torch.zeros(256, dtype=torch.uint8))
+    assert grads.dx_perm is mine
