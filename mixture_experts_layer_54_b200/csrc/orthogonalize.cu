@@ -307,12 +307,12 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     const int esz = bf16 ? 2 : 4;
     const bool al = (reinterpret_cast<uintptr_t>(G) & 15u) == 0;
     const int64_t want = ceil_div(mn, 256 * 8 * 4);
-    const int64_t cap = ceil_div(148 * 6, E);   // a few blocks an SM over all matrices
+    const int64_t cap = ceil_div(device_sms() * 6, E);   // a few blocks an SM over all matrices
     const int64_t most_parts = cap < kMaxParts ? cap : kMaxParts;
     const int parts = (int)(want < 1 ? 1 : (want > most_parts ? most_parts : want));
     const bool vsum = al && mn * esz % 16 == 0, vrow = al && (int64_t)n * esz % 16 == 0;
     int64_t cblocks = ceil_div((int64_t)m * (ldx / 8), 256);
-    const int64_t most = ceil_div(148 * 16, E);
+    const int64_t most = ceil_div(device_sms() * 16, E);
     cblocks = cblocks > most ? most : cblocks;
     // X0 needs its low half unless G is bf16 (exact in one term) or this is the only step
     const bool lo0 = !bf16 && steps > 1;
