@@ -86,6 +86,35 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, const int32_t
     *count = rows ? min(max(rows[g], 0), hi - lo) : hi - lo;
 }
 
+// MN-major operand, 128-byte swizzle: 64 contiguous elements per 128-byte row,
+// one row per contraction index; 8-row groups 1024 bytes apart (stride offset),
+// blocks of 64 elements `block` bytes apart (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate)
+{
+    if (CTAS == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
 // Epilogues: EPI_ROWS bf16 rows; EPI_DW fp32 or bf16 with an addend; EPI_NS
 // the Newton-Schulz stores; EPI_GELU / EPI_SWIGLU the hidden activations and
 // their gradients.  EPI_ROWS_LONG is launch_tc's own choice for EPI_ROWS.

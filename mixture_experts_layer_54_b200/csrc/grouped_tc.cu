@@ -263,35 +263,6 @@ __device__ __forceinline__ bool ragged_tail(int rem)
     return rem < BK && (rem & 15);
 }
 
-// MN-major operand, 128-byte swizzle: 64 contiguous elements per 128-byte row,
-// one row per contraction index; 8-row groups 1024 bytes apart (stride offset),
-// blocks of 64 elements `block` bytes apart (leading offset).
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block)
-{
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-template <int CTAS>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                    uint32_t accumulate)
-{
-    if (CTAS == 2)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
-
 template <int CTAS>
 __device__ __forceinline__ void commit_all(uint32_t bar)
 {
@@ -1284,6 +1255,10 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                     //   GELU    h = u Phi(u); du = dh (Phi(u) + u phi(u))
                     //   SwiGLU  h = u s v, s = 1 / (1 + e^-u);
                     //           du = dh v s (1 + u (1 - s)), dv = dh u s
+                    // h, du and dv are rounded to bf16 here, as the forward rounds its h: they
+                    // are the next products' operands on the tensor cores.  Against 64 bits
+                    // the gradients are off by 2.4e-3 (2-norm); held in fp32 until the end
+                    // they would be by 1.7e-3, at twice the products that take them.
                     const uint32_t tu = tq + c + (EPI == EPI_GELU ? slot * 2 * BN : 0);
                     const uint32_t tdh = tq + c + S::DH_COL + slot * (EPI == EPI_GELU ? 2 * BN : BN);
                     float dh[32];

@@ -37,13 +37,6 @@ constexpr int kMaxParts = 256;
 
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-
 // 8 consecutive elements from p (`vec`: p is 16-byte aligned), n of them valid
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, int n, bool vec, float *f)

@@ -3,6 +3,7 @@
 // step), so that neither end of fp16's range is near.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <math.h>
 
 namespace moe {
@@ -29,6 +30,13 @@ __device__ __forceinline__ int x_shift(float u)
     return (int)fminf(floorf(-log2f(u)), 100.f);
 }
 __device__ __forceinline__ float power2(int k) { return __int_as_float((127 + k) << 23); }
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 }  // namespace grp
 }  // namespace moe

@@ -45,26 +45,6 @@ __device__ __forceinline__ uint32_t place(int row, int col)
            (col & 7) * 2;
 }
 
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) { return sdesc_sw128(saddr); }
-
-// MN-major: blocks of 64 columns BLOCK bytes apart, 8-row groups 1024
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr)
-{
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(BLOCK >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                    uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // 16 values of a row, as hi + lo, to columns col .. col + 15 of both terms
 __device__ __forceinline__ void put16(uint8_t *hi, uint8_t *lo, int row, int col, const float *v)
 {
@@ -105,13 +85,6 @@ __device__ __forceinline__ void get16(const uint8_t *hi, const uint8_t *lo, int 
         }
     }
 }
-
-template <typename T>
-__device__ __forceinline__ float as_float(T v);
-template <>
-__device__ __forceinline__ float as_float(float v) { return v; }
-template <>
-__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 __host__ __device__ constexpr uint32_t tmem_cols(int blocks) { return blocks <= 2 ? 256 : 512; }
 
@@ -163,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
         float f[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            f[u] = i + u * THREADS < mn ? as_float<T>(G[i + u * THREADS]) : 0.f;
+            f[u] = i + u * THREADS < mn ? to_f<T>(G[i + u * THREADS]) : 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             acc[u] = fmaf(f[u], f[u], acc[u]);
@@ -194,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     if (again) {
         double w = 0;
         for (int i = tid; i < mn; i += THREADS) {
-            const double x = (double)as_float<T>(G[i]);
+            const double x = (double)to_f<T>(G[i]);
             w += x * x;
         }
         warp_sums(w);
@@ -219,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
     for (int i = tid; i < mn; i += THREADS) {
         const int r = i / s.n, c = i - r * s.n;
         const uint32_t o = wide ? place(r, c) : place(c, r);
-        const float x = as_float<T>(G[i]) * mul * over;
+        const float x = to_f<T>(G[i]) * mul * over;
         const __half h = __float2half_rn(x);
         *reinterpret_cast<__half *>(xh + o) = h;
         *reinterpret_cast<__half *>(xl + o) = __float2half_rn(x - __half2float(h));
@@ -257,7 +230,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
         for (int term = 0; term < 3; ++term)
             for (int k = 0; k < steps; ++k) {
                 const uint32_t o = (uint32_t)(k >> 2) * BLOCK + (k & 3) * 32;
-                mma(d, desc_k(t[term == 2] + o), desc_k(t[term == 1] + o), id, first ? 0u : 1u);
+                mma<1>(d, sdesc_sw128(t[term == 2] + o), sdesc_sw128(t[term == 1] + o), id,
+                       first ? 0u : 1u);
                 first = false;
             }
         mma_commit(bar);
@@ -311,8 +285,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_small_kernel(const SmallParams 
                     for (int k = 0; k < pk; ++k) {
                         const uint32_t oa = (uint32_t)(k >> 2) * BLOCK + (k & 3) * 32;
                         const uint32_t ob = (uint32_t)n0 * BLOCK + k * 2048;
-                        mma(t_x + n0 * 64, desc_k(as[term == 2] + oa), desc_mn(ax[term == 1] + ob),
-                            id, first ? 0u : 1u);
+                        mma<1>(t_x + n0 * 64, sdesc_sw128(as[term == 2] + oa),
+                               sdesc_mn(ax[term == 1] + ob, BLOCK), id, first ? 0u : 1u);
                         first = false;
                     }
             }
