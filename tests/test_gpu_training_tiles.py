@@ -4,7 +4,7 @@ that a changed choice cannot leave one untested.
 
 Kernels are grouped_kernel<CTAs, columns, A across its rows, B across its rows,
 epilogue, rows a CTA, sets>; epilogues: 0 rows, 1 weight gradient, 2 Newton-Schulz,
-3 GELU and 4 SwiGLU hidden gradients.
+3 GELU and 4 SwiGLU hidden gradients, 5 rows over a long contraction.
 """
 import re
 
@@ -68,6 +68,31 @@ def test_products_on_pairs_of_sms(aligned, wide):
             within(got[lo:hi], r, 2.0 ** -8 * r.abs() + K * 2.0 ** -23 * (a.abs() @ w.abs()))
         r = b.T @ a
         within(dW[g], r, 2.0 ** -24 * r.abs() + (hi - lo + 1) * 2.0 ** -23 * (b.abs().T @ a.abs()))
+
+
+@pytest.mark.parametrize("N,K,epi", [(264, 3000, 0), (520, 320, 0), (136, 8200, 5), (1160, 4160, 5)])
+def test_few_rows_on_tiles_of_32(N, K, epi):
+    """Groups below, at and just past 32 rows, whole tiles and cut ones, in one
+    accumulator and in several."""
+    off, _, R, spans = table([20, 0, 9, 33, 2, 32, 1, 5, 16, 7], False)
+    x, dy = randn(R, K, seed=1), randn(R, K, seed=2)
+    inside = torch.zeros(R, dtype=torch.bool, device="cuda")
+    for lo, hi in spans:
+        inside[lo:hi] = True
+    x[~inside] = float("nan")
+    dy[~inside] = float("nan")
+    W = randn(10, N, K, seed=3, scale=K ** -0.5)
+    Wx = randn(10, K, N, seed=4, scale=K ** -0.5)
+    y, dx = (torch.full((R, N), 7.0, dtype=BF, device="cuda") for _ in range(2))
+    _, kind = launched(lambda: moe.moe_grouped_matmul(x, W, off, y=y))
+    assert kind == [(1, 128, 0, 0, epi, 32, 1)]
+    _, kind = launched(lambda: moe.moe_grouped_matmul_dx(dy, Wx, off, dx=dx))
+    assert kind == [(1, 128, 0, 1, epi, 32, 1)]
+    assert (y[~inside] == 7.0).all() and (dx[~inside] == 7.0).all()
+    for g, (lo, hi) in enumerate(spans):
+        for got, a, w in ((y, x[lo:hi].to(F64), W[g].to(F64).T), (dx, dy[lo:hi].to(F64), Wx[g].to(F64))):
+            r = a @ w
+            within(got[lo:hi], r, 2.0 ** -8 * r.abs() + K * 2.0 ** -23 * (a.abs() @ w.abs()))
 
 
 FFN = {
