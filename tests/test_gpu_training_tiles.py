@@ -108,6 +108,19 @@ FFN = {
     "swiglu_pairs_alone": (8, RAGGED, 1344, 320, 1, 0, 0,
                            [(2, 128, 0, 0, 4, 128, 2), (2, 256, 0, 1, 0, 128, 1),
                             (2, 256, 1, 1, 1, 128, 6)]),
+    # du W1 + dv W3 past 4096 of contraction
+    "swiglu_long_single": (4, [90, 70, 40, 33], 64, 2112, 1, 1, 64,
+                           [(2, 128, 0, 0, 4, 128, 2), (1, 128, 0, 1, 5, 128, 2),
+                            (1, 128, 1, 1, 1, 128, 6)]),
+    "gelu_long_pairs": (8, RAGGED, 1344, 4160, 0, 2, 64,
+                        [(2, 128, 0, 0, 3, 128, 2), (2, 256, 0, 1, 5, 128, 2),
+                         (2, 256, 1, 1, 1, 128, 6)]),
+    "swiglu_long_pairs_alone": (8, RAGGED, 1344, 2112, 1, 0, 0,
+                                [(2, 128, 0, 0, 4, 128, 2), (2, 256, 0, 1, 5, 128, 1),
+                                 (2, 256, 1, 1, 1, 128, 6)]),
+    "gelu_long_single_alone": (4, [90, 70, 40, 33], 64, 4160, 0, 0, 0,
+                               [(1, 128, 0, 0, 3, 128, 2), (1, 128, 0, 1, 5, 128, 1),
+                                (1, 128, 1, 1, 1, 128, 6)]),
 }
 
 
