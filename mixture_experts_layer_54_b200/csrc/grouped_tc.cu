@@ -27,10 +27,10 @@
 // where fp32 rounding alone leaves 3e-7), so a weight gradient over many rows
 // is summed in accumulators of 512 rows each, which the epilogue adds up in
 // registers (round to nearest) while the next one fills: 128 values a thread.
-// Products and input gradients, which end in bf16, take accumulators of 4096 (5e-6;
-// a single one left 2e-5 at 14336 and 1e-3 at 2^20), in kernels of their own: with
-// the sums' registers the short contractions took 2 to 5% longer.  u, v and dh (over
-// the layer's width) and the stacks keep a single one.
+// Products and input gradients, which end in bf16, take accumulators of 8192 past
+// that (1e-5; a single one left 2e-5 at 14336 and 1e-3 at 2^20), in kernels of their
+// own: with the sums' code and registers contractions of 256 to 8192 took 2 to 5%
+// longer.  u, v and dh (over the layer's width) and the stacks keep a single one.
 //
 // Work is dealt as tiles, one to each CTA (pair) in turn.  Where the last round
 // would leave most of them idle (or, with few rows, every round), the tiles of
@@ -71,7 +71,7 @@ constexpr int EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int STG_WARP = 32 * 64;        // staging tile of an epilogue warp: 32 rows of 64 bytes
 constexpr int RING_BYTES = 192 * 1024;
-constexpr int kLongRows = 4096;          // EPI_ROWS_LONG: contraction in one accumulator
+constexpr int kLongRows = 8192;          // EPI_ROWS_LONG: contraction in one accumulator
 
 // AR: rows of A a CTA takes, 128, or 32 for groups of few rows: the MMA's other
 // rows read on into the next bytes of the ring, their results are never stored,
@@ -299,7 +299,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
 // Arrive on the leader's barrier with `bytes` to come by TMA.  Nothing this
 // thread wrote has to be seen by the waiter, so the arrival is relaxed (with a
 // release at cluster scope for every stage 16384 rows through 8 x 4096 x 14336
-// took 2152 us instead of 1287).
+// took 1820 us instead of 1390).
 template <int CTAS>
 __device__ __forceinline__ void arrive_bytes(uint32_t bar, uint32_t bytes)
 {
@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(Shape<CTAS, BN, EPI, AR>::THREADS, 1)
                             ((int64_t)t.cut * t.parts + t.part) * part_step +
                             (int64_t)wid * (BN / 8) * 32;
             unsigned long long *count = p.counters + t.cut * (CTAS * S::ROW_WARPS) + wid;
-            if (EPI == EPI_DW || (S::CHUNK > 0 && t.b1 - t.b0 > S::CHUNK_BLOCKS)) {
+            if constexpr (S::CHUNK > 0) {
                 float sum[BN / 2];
                 if (t.b0 == t.b1) {   // nothing was accumulated: an empty group's sum
 #pragma unroll

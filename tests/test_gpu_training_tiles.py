@@ -70,7 +70,7 @@ def test_products_on_pairs_of_sms(aligned, wide):
         within(dW[g], r, 2.0 ** -24 * r.abs() + (hi - lo + 1) * 2.0 ** -23 * (b.abs().T @ a.abs()))
 
 
-@pytest.mark.parametrize("N,K,epi", [(264, 3000, 0), (520, 320, 0), (136, 8200, 5), (1160, 4160, 5)])
+@pytest.mark.parametrize("N,K,epi", [(264, 3000, 0), (520, 320, 0), (136, 8200, 5), (1160, 8264, 5)])
 def test_few_rows_on_tiles_of_32(N, K, epi):
     """Groups below, at and just past 32 rows, whole tiles and cut ones, in one
     accumulator and in several."""
@@ -108,17 +108,17 @@ FFN = {
     "swiglu_pairs_alone": (8, RAGGED, 1344, 320, 1, 0, 0,
                            [(2, 128, 0, 0, 4, 128, 2), (2, 256, 0, 1, 0, 128, 1),
                             (2, 256, 1, 1, 1, 128, 6)]),
-    # du W1 + dv W3 past 4096 of contraction
-    "swiglu_long_single": (4, [90, 70, 40, 33], 64, 2112, 1, 1, 64,
-                           [(2, 128, 0, 0, 4, 128, 2), (1, 128, 0, 1, 5, 128, 2),
+    # du W1 + dv W3 past 8192 of contraction
+    "swiglu_long_single": (4, [90, 70, 40, 33], 64, 4160, 1, 1, 64,
+                           [(1, 128, 0, 0, 4, 128, 2), (1, 128, 0, 1, 5, 128, 2),
                             (1, 128, 1, 1, 1, 128, 6)]),
-    "gelu_long_pairs": (8, RAGGED, 1344, 4160, 0, 2, 64,
+    "gelu_long_pairs": (8, RAGGED, 1344, 8256, 0, 2, 64,
                         [(2, 128, 0, 0, 3, 128, 2), (2, 256, 0, 1, 5, 128, 2),
                          (2, 256, 1, 1, 1, 128, 6)]),
-    "swiglu_long_pairs_alone": (8, RAGGED, 1344, 2112, 1, 0, 0,
+    "swiglu_long_pairs_alone": (8, RAGGED, 1344, 4160, 1, 0, 0,
                                 [(2, 128, 0, 0, 4, 128, 2), (2, 256, 0, 1, 5, 128, 1),
                                  (2, 256, 1, 1, 1, 128, 6)]),
-    "gelu_long_single_alone": (4, [90, 70, 40, 33], 64, 4160, 0, 0, 0,
+    "gelu_long_single_alone": (4, [90, 70, 40, 33], 64, 8256, 0, 0, 0,
                                [(1, 128, 0, 0, 3, 128, 2), (1, 128, 0, 1, 5, 128, 1),
                                 (1, 128, 1, 1, 1, 128, 6)]),
 }
