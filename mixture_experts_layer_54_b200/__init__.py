@@ -18,9 +18,11 @@ from .ops import (CapacityOut, HostStream, MoEForward, moe_bias_update, moe_capa
                   StagedForward,
                   workspace)
 from .training import (FFNGrads, moe_clear_training_status, moe_combine_backward,
-                       moe_expert_ffn_backward, moe_probe_training_timeout, moe_training_status,
-                       moe_ffn_backward_workspace_size, moe_grouped_matmul, moe_grouped_matmul_dw,
-                       moe_grouped_matmul_dx, moe_orthogonalize, moe_orthogonalize_workspace_size)
+                       moe_expert_ffn_backward, moe_ffn_backward_workspace_size,
+                       moe_grouped_matmul, moe_grouped_matmul_dw, moe_grouped_matmul_dx,
+                       moe_grouped_workspace_size, moe_orthogonalize,
+                       moe_orthogonalize_workspace_size, moe_probe_training_timeout,
+                       moe_training_status)
 
 __all__ = ["MOE_ROW_ALIGN", "CapacityFactorError", "MoEError", "MoeConfig", "MoeOutputs",
            "MoeWeights", "LIB_PATH", "lib", "CapacityOut", "HostStream", "MoEForward", "moe_bias_update",
@@ -35,4 +37,4 @@ __all__ = ["MOE_ROW_ALIGN", "CapacityFactorError", "MoEError", "MoeConfig", "Moe
            "moe_expert_ffn_backward", "moe_ffn_backward_workspace_size", "moe_grouped_matmul",
            "moe_grouped_matmul_dw", "moe_grouped_matmul_dx", "moe_orthogonalize",
            "moe_orthogonalize_workspace_size", "moe_training_status", "moe_clear_training_status",
-           "moe_probe_training_timeout"]
+           "moe_probe_training_timeout", "moe_grouped_workspace_size"]

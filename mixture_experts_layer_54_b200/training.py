@@ -85,6 +85,11 @@ def _workspace(nbytes, like):
     return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
 
 
+def moe_grouped_workspace_size(dtype, G: int, R: int, N: int, K: int) -> int:
+    """Bytes of the workspace of the three grouped products; 0 for sizes they refuse."""
+    return int(lib().moe_grouped_workspace_size(_CODES.get(dtype, -1), int(G), int(R), int(N), int(K)))
+
+
 _grouped_bytes = 0
 
 
@@ -293,7 +298,8 @@ def moe_probe_training_timeout(timeout_ns: int):
           "moe_probe_training_timeout")
 
 
-__all__ = ["moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
-           "moe_combine_backward", "moe_expert_ffn_backward", "moe_ffn_backward_workspace_size",
-           "FFNGrads", "moe_orthogonalize", "moe_orthogonalize_workspace_size", "moe_training_status",
+__all__ = ["moe_grouped_workspace_size", "moe_grouped_matmul", "moe_grouped_matmul_dx",
+           "moe_grouped_matmul_dw", "moe_combine_backward", "moe_expert_ffn_backward",
+           "moe_ffn_backward_workspace_size", "FFNGrads", "moe_orthogonalize",
+           "moe_orthogonalize_workspace_size", "moe_training_status",
            "moe_clear_training_status", "moe_probe_training_timeout"]

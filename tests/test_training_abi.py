@@ -175,6 +175,13 @@ def test_orthogonalize_refuses_steps_that_leave_fp16(coeffs, steps):
         assert status == _abi.MOE_ERR_SHAPE
 
 
+def test_grouped_workspace_size_of_the_binding():
+    size = moe.moe_grouped_workspace_size
+    assert size(torch.bfloat16, 4, 100, 64, 64) == moe.lib().moe_grouped_workspace_size(BF16, 4, 100, 64, 64)
+    assert size(torch.bfloat16, 4, 100, 60, 64) == 0 and size(torch.float32, 4, 100, 60, 64) >= 256
+    assert size(torch.float16, 4, 100, 64, 64) == 0
+
+
 def test_training_status_checks_its_arguments():
     assert moe.lib().moe_training_status(None, None) == _abi.MOE_ERR_NULL
     assert moe.lib().moe_probe_training_timeout(2_000_000_001, None) == _abi.MOE_ERR_SHAPE
