@@ -592,10 +592,11 @@ size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t
  *   steps <= 32.  A matrix of zeros gives zeros (NaN when eps is 0); one with an
  *   infinity or NaN gives NaN, in its own update only.
  * The products take fp16 operands (X itself is held as two fp16 terms): the
- * result is that of 64-bit arithmetic within about 2e-3 (relative, 2-norm) after
- * five steps, for |G| far below eps too (down to 1e-24 of it), then rounded to bf16.
- * (5.5e-3 after 32 steps of the quintic, which does not settle.)  Up to 128 x 320
- * every operand is two fp16 terms: within 1e-5.
+ * result is that of 64-bit arithmetic within about 2e-3 (relative, 2-norm; 3e-3 where
+ * singular values are equal) after five steps, for |G| far below eps too (down to
+ * 1e-24 of it), then rounded to bf16.  (5.5e-3 after 32 steps of the quintic, which
+ * does not settle.)  Up to 128 x 320, where every operand is two fp16 terms, and for
+ * m or n up to 56, where the steps run in double: within 1e-4.
  */
 moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, const void *G,
                              int32_t steps, const float *coeffs, float eps, float scale, void *U,

@@ -278,10 +278,18 @@ cudaError_t launch_orthogonalize_small(bool bf16, int E, int m, int n, const voi
                                        float a, float b, float c, float eps, float scale, void *U,
                                        int32_t *status, cudaStream_t s);
 
+bool orthogonalize_is_gram(int m, int n);
+size_t orthogonalize_gram_bytes(int64_t E, int m, int n);
+cudaError_t launch_orthogonalize_gram(bool bf16, int E, int m, int n, const void *G, int steps,
+                                      float a, float b, float c, float eps, float scale, void *U,
+                                      void *ws, cudaStream_t s);
+
 size_t orthogonalize_bytes(int64_t E, int64_t m, int64_t n, int steps)
 {
     if (orthogonalize_is_small((int)m, (int)n))
         return 256;   // the status word alone
+    if (orthogonalize_is_gram((int)m, (int)n))
+        return orthogonalize_gram_bytes(E, (int)m, (int)n);
     return carve(E, m, n, steps, nullptr).bytes;
 }
 
@@ -292,6 +300,8 @@ cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, 
     if (orthogonalize_is_small(m, n))
         return launch_orthogonalize_small(bf16, E, m, n, G, steps, a, b, c, eps, scale, U,
                                           static_cast<int32_t *>(ws), s);
+    if (orthogonalize_is_gram(m, n))
+        return launch_orthogonalize_gram(bf16, E, m, n, G, steps, a, b, c, eps, scale, U, ws, s);
     Bufs w = carve(E, m, n, steps, ws);
     const int64_t mn = (int64_t)m * n, ldx = up8(n);
     const bool wide = m <= n;

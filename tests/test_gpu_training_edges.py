@@ -137,7 +137,7 @@ PROMISED = 2e-3 + 2.0 ** -8
 CUBIC = (1.5, -0.5, 0.0)
 
 
-@pytest.mark.parametrize("m,n", [(48, 80), (90, 40), (300, 700), (520, 264)])
+@pytest.mark.parametrize("m,n", [(48, 80), (90, 40), (300, 700), (520, 264), (8, 700), (900, 33)])
 @pytest.mark.parametrize("steps,coeffs,tol", [(1, QUINTIC, PROMISED), (2, QUINTIC, PROMISED),
                                               (5, QUINTIC, PROMISED), (30, CUBIC, NS_TOL)])
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -157,7 +157,7 @@ def test_orthogonalize_far_below_eps(m, n, steps, coeffs, tol, dtype):
 
 @pytest.mark.parametrize("coeffs,steps,last", [((2.79, 0.0, 0.0), 2, 2.79 ** 2), ((1.0, 29.5, 0.0), 1, 30.5),
                                                ((0.0, 0.0, 1.3), 2, 1.3 ** 6), ((-30.9, 0.0, 0.0), 1, -30.9)])
-@pytest.mark.parametrize("m,n", [(40, 64), (300, 264)])
+@pytest.mark.parametrize("m,n", [(40, 64), (300, 264), (20, 600)])
 def test_orthogonalize_at_the_edge_of_its_range(coeffs, steps, last, m, n):
     """Coefficients just inside what is refused, on a matrix of one singular value,
     which the norm makes 1: nothing overflows.  (X, B and the product: each operand
@@ -228,3 +228,62 @@ def test_a_wait_that_ran_out_is_not_lost_with_its_workspace():
     assert torch.equal(moe.moe_grouped_matmul(x, W, off)[3:103], y[3:103])
     assert torch.equal(moe.moe_orthogonalize(G), U)
     assert moe.moe_training_status() == 0
+
+
+LONG_AND_NARROW = [(4, 637), (637, 4), (1, 5000), (5000, 1), (17, 330), (56, 4096), (1001, 55), (330, 33),
+                   (2, 100001), (9, 321), (16, 2049), (513, 32)]
+
+
+@pytest.mark.parametrize("kind", ["noise", "rank_32", "decaying", "equal"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n", LONG_AND_NARROW)
+def test_orthogonalize_of_few_rows_or_columns(m, n, dtype, kind):
+    """Up to 56 rows or columns, longer than one block holds: singular values that lie
+    together (all of them, or equal) are no worse than others.  The last product is in
+    fp32: P, up to 485 after five steps, times X, at 2^-24 each and a few of them."""
+    E = 5
+    if kind == "equal":
+        g = torch.Generator(device="cuda")
+        g.manual_seed(m + n)
+        G = torch.linalg.qr(torch.randn((E, max(m, n), min(m, n)), generator=g, device="cuda"))[0]
+        G = (G if m > n else G.mT).to(dtype).contiguous()
+    else:
+        G = update(kind, E, m, n, dtype)
+    ws = moe.workspace(moe.moe_orthogonalize_workspace_size(E, m, n), "cuda")
+    ws.fill_(255)
+    U, ref = moe.moe_orthogonalize(G, ws=ws).to(F64), newton_schulz(G, 5, QUINTIC)
+    assert moe.moe_device_status(ws) == 0
+    half = half_step(ref)
+    for e in range(E):
+        over = ((U[e] - ref[e]).abs() - half[e]).clamp(min=0).norm() / ref[e].norm()
+        assert over.item() <= 2e-4, (e, over.item())
+
+
+@pytest.mark.parametrize("m,n", [(7, 700), (700, 7), (50, 400), (57, 400)])
+def test_few_rows_or_columns_of_zeros_infinities_and_far_magnitudes(m, n):
+    G = randn(6, m, n, seed=1, dtype=F32)
+    G[1] = 0
+    G[2, 3, 4] = float("inf")
+    G[3] *= 2.0 ** -130
+    G[4] *= 2.0 ** 110
+    U = moe.moe_orthogonalize(G, eps=0.0)
+    assert torch.isnan(U[1]).all() and torch.isnan(U[2]).all()
+    ref = newton_schulz(G, 5, QUINTIC, eps=0.0)
+    tol = 2.0 ** -8 + (1e-4 if min(m, n) <= 56 else 16 * 2.0 ** -11)   # as NS_TOL
+    for e in (0, 3, 4, 5):
+        assert ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item() <= tol
+    assert (moe.moe_orthogonalize(G[1:2]) == 0).all()
+    # one matrix, in and out off the 16-byte grid; scale; one step and many; a replay
+    size = m * n
+    flat, out = (torch.zeros(size + 1, dtype=BF, device="cuda") for _ in range(2))
+    flat[1:] = G[0].reshape(-1).to(BF)
+    one = flat[1:].view(m, n)
+    for steps, coeffs, scale in ((1, QUINTIC, 1.0), (5, QUINTIC, 0.3), (30, CUBIC, 1.0)):
+        got = moe.moe_orthogonalize(one, steps=steps, coeffs=coeffs, scale=scale, U=out[1:].view(m, n))
+        ref = scale * newton_schulz(one, steps, coeffs)
+        assert ((got.to(F64) - ref).norm() / ref.norm()).item() <= tol
+        graph, again, _ = capture(lambda: moe.moe_orthogonalize(one, steps=steps, coeffs=coeffs, scale=scale))
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, got)
