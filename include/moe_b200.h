@@ -596,7 +596,8 @@ size_t moe_orthogonalize_workspace_size(int32_t E, int32_t m, int32_t n, int32_t
  * singular values are equal) after five steps, for |G| far below eps too (down to
  * 1e-24 of it), then rounded to bf16.  (5.5e-3 after 32 steps of the quintic, which
  * does not settle.)  Up to 128 x 320, where every operand is two fp16 terms, and for
- * m or n up to 56, where the steps run in double: within 1e-4.
+ * m or n up to 56 and at most six steps of the quintic (|a|^steps <= 2048), where the
+ * steps run in double: within 1e-4.
  */
 moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, const void *G,
                              int32_t steps, const float *coeffs, float eps, float scale, void *U,

@@ -278,7 +278,7 @@ cudaError_t launch_orthogonalize_small(bool bf16, int E, int m, int n, const voi
                                        float a, float b, float c, float eps, float scale, void *U,
                                        int32_t *status, cudaStream_t s);
 
-bool orthogonalize_is_gram(int m, int n);
+bool orthogonalize_is_gram(int m, int n, double growth);
 size_t orthogonalize_gram_bytes(int64_t E, int m, int n);
 cudaError_t launch_orthogonalize_gram(bool bf16, int E, int m, int n, const void *G, int steps,
                                       float a, float b, float c, float eps, float scale, void *U,
@@ -288,19 +288,21 @@ size_t orthogonalize_bytes(int64_t E, int64_t m, int64_t n, int steps)
 {
     if (orthogonalize_is_small((int)m, (int)n))
         return 256;   // the status word alone
-    if (orthogonalize_is_gram((int)m, (int)n))
-        return orthogonalize_gram_bytes(E, (int)m, (int)n);
-    return carve(E, m, n, steps, nullptr).bytes;
+    const size_t bytes = carve(E, m, n, steps, nullptr).bytes;
+    // the coefficients decide between the two
+    const size_t gram = orthogonalize_is_gram((int)m, (int)n, 1)
+                            ? orthogonalize_gram_bytes(E, (int)m, (int)n) : 0;
+    return bytes > gram ? bytes : gram;
 }
 
 cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, int steps,
-                                 float a, float b, float c, float eps, float scale, void *U,
-                                 void *ws, cudaStream_t s)
+                                 float a, float b, float c, double growth, float eps, float scale,
+                                 void *U, void *ws, cudaStream_t s)
 {
     if (orthogonalize_is_small(m, n))
         return launch_orthogonalize_small(bf16, E, m, n, G, steps, a, b, c, eps, scale, U,
                                           static_cast<int32_t *>(ws), s);
-    if (orthogonalize_is_gram(m, n))
+    if (orthogonalize_is_gram(m, n, growth))
         return launch_orthogonalize_gram(bf16, E, m, n, G, steps, a, b, c, eps, scale, U, ws, s);
     Bufs w = carve(E, m, n, steps, ws);
     const int64_t mn = (int64_t)m * n, ldx = up8(n);

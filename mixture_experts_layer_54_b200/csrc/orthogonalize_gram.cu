@@ -275,8 +275,14 @@ GramBufs carve(int64_t E, int m, int n, void *ws)
 }  // namespace
 
 // What the stacked products cannot hold to 2e-3; from 57 on they do, and are the
-// faster of the two.
-bool orthogonalize_is_gram(int m, int n) { return (m < n ? m : n) <= 56; }
+// faster of the two.  growth: P is held in fp32 for the last product, so where a
+// singular value is zero the result is off by growth 2^-24; the quintic's six steps
+// are 1670.  (X itself, which the stacked products keep, stays bounded however many
+// steps there are.)
+bool orthogonalize_is_gram(int m, int n, double growth)
+{
+    return (m < n ? m : n) <= 56 && growth <= 2048;
+}
 
 size_t orthogonalize_gram_bytes(int64_t E, int m, int n) { return carve(E, m, n, nullptr).bytes; }
 

@@ -16,8 +16,8 @@ cudaError_t launch_combine_grad(const moe_config &c, const void *dy, const void 
 namespace grp {
 size_t orthogonalize_bytes(int64_t E, int64_t m, int64_t n, int steps);
 cudaError_t launch_orthogonalize(bool bf16, int E, int m, int n, const void *G, int steps, float a,
-                                 float b, float c, float eps, float scale, void *U, void *ws,
-                                 cudaStream_t s);
+                                 float b, float c, double growth, float eps, float scale, void *U,
+                                 void *ws, cudaStream_t s);
 // The words that say that a bounded wait ran out on this device.
 cudaError_t gave_up_grouped(int32_t **word);
 cudaError_t gave_up_small(int32_t **word);
@@ -273,10 +273,12 @@ moe_status rows_call(int32_t dtype, int32_t G, int64_t R, int32_t N, int32_t K, 
 // Whether every X, X X^T and a I + b A + c A A of `steps` steps stays inside fp16 as
 // they are stored (times 8192, 8192 and 2048), for singular values from 0 to 1 at
 // the start: p(x) = x g(x^2), g(s) = a + b s + c s^2, at the ends of the interval and
-// where p' or g' is zero.
-bool steps_in_range(double a, double b, double c, int steps)
+// where p' or g' is zero.  *growth: the most that all steps together multiply a
+// singular value by.
+bool steps_in_range(double a, double b, double c, int steps, double *growth)
 {
     double u = 1;
+    *growth = 1;
     for (int i = 0; i < steps; ++i) {
         if (!(u <= 2.8))   // 8192 u^2 <= 64225
             return false;
@@ -296,6 +298,7 @@ bool steps_in_range(double a, double b, double c, int steps)
         look(-a / (3 * b));                              // c = 0
         if (!(most <= 31))   // 2048 g <= 63488
             return false;
+        *growth *= most;
         u = top;
     }
     return true;
@@ -716,10 +719,11 @@ moe_status moe_orthogonalize(int32_t dtype, int32_t E, int32_t m, int32_t n, con
     const moe_status st = check_ws(ws, ws_bytes, need);
     if (st != MOE_OK)
         return st;
-    if (!steps_in_range(coeffs[0], coeffs[1], coeffs[2], steps))
+    double growth;
+    if (!steps_in_range(coeffs[0], coeffs[1], coeffs[2], steps, &growth))
         return MOE_ERR_SHAPE;
     return cuda_status(launch_orthogonalize(dtype == MOE_DTYPE_BF16, E, m, n, G, steps, coeffs[0],
-                                            coeffs[1], coeffs[2], eps, scale, U, ws,
+                                            coeffs[1], coeffs[2], growth, eps, scale, U, ws,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -259,6 +259,19 @@ def test_orthogonalize_of_few_rows_or_columns(m, n, dtype, kind):
         assert over.item() <= 2e-4, (e, over.item())
 
 
+@pytest.mark.parametrize("m,n", [(8, 700), (700, 8), (50, 400), (40, 60), (300, 520)])
+@pytest.mark.parametrize("steps,coeffs", [(6, QUINTIC), (7, QUINTIC), (32, QUINTIC), (32, CUBIC)])
+def test_orthogonalize_of_low_rank_by_many_steps(m, n, steps, coeffs):
+    """Directions that G does not have are multiplied by a in every step, whatever the
+    rounding left there: with more steps than precision they come out as singular
+    values near 1, never larger.  (The quintic's stay below 1.21, the cubic's below 1;
+    a singular value past 1.25 is an overflow on its way.)"""
+    G = randn(3, m, 2, seed=1, dtype=F32) @ randn(3, 2, n, seed=2, dtype=F32)
+    U = moe.moe_orthogonalize(G, steps=steps, coeffs=coeffs)
+    assert torch.isfinite(U).all()
+    assert torch.linalg.svdvals(U.to(F64)).max().item() <= 1.25
+
+
 @pytest.mark.parametrize("m,n", [(7, 700), (700, 7), (50, 400), (57, 400)])
 def test_few_rows_or_columns_of_zeros_infinities_and_far_magnitudes(m, n):
     G = randn(6, m, n, seed=1, dtype=F32)
@@ -269,7 +282,8 @@ def test_few_rows_or_columns_of_zeros_infinities_and_far_magnitudes(m, n):
     U = moe.moe_orthogonalize(G, eps=0.0)
     assert torch.isnan(U[1]).all() and torch.isnan(U[2]).all()
     ref = newton_schulz(G, 5, QUINTIC, eps=0.0)
-    tol = 2.0 ** -8 + (1e-4 if min(m, n) <= 56 else 16 * 2.0 ** -11)   # as NS_TOL
+    close, far = 2.0 ** -8 + 1e-4, NS_TOL
+    tol = close if min(m, n) <= 56 else far
     for e in (0, 3, 4, 5):
         assert ((U[e].to(F64) - ref[e]).norm() / ref[e].norm()).item() <= tol
     assert (moe.moe_orthogonalize(G[1:2]) == 0).all()
@@ -281,7 +295,8 @@ def test_few_rows_or_columns_of_zeros_infinities_and_far_magnitudes(m, n):
     for steps, coeffs, scale in ((1, QUINTIC, 1.0), (5, QUINTIC, 0.3), (30, CUBIC, 1.0)):
         got = moe.moe_orthogonalize(one, steps=steps, coeffs=coeffs, scale=scale, U=out[1:].view(m, n))
         ref = scale * newton_schulz(one, steps, coeffs)
-        assert ((got.to(F64) - ref).norm() / ref.norm()).item() <= tol
+        many = coeffs[0] ** steps > 2048
+        assert ((got.to(F64) - ref).norm() / ref.norm()).item() <= (far if many else tol)
         graph, again, _ = capture(lambda: moe.moe_orthogonalize(one, steps=steps, coeffs=coeffs, scale=scale))
         again.zero_()
         graph.replay()
